@@ -35,7 +35,9 @@ EXPORTS = ("pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_
            "pq_quantize_fwd", "pq_quantize_bwd", "pq_pack_w2", "pq_pack_w4", "pq_w2a16_gemm",
            "pq_w4a16_gemm", "pq_quantize_fwd_grouped", "pq_quantize_bwd_grouped", "pq_qat_step",
            "pq_qat_step_grouped", "pq_pack", "pq_gemm", "pq_gemm_f32a", "pq_num_levels", "pq_level_stats",
-           "pq_quantize_fwd_stats", "pq_weight_movement", "pq_pack_grouped", "pq_gemm_noalloc")
+           "pq_quantize_fwd_stats", "pq_weight_movement", "pq_pack_grouped", "pq_gemm_noalloc",
+           "pq_rope_table", "pq_rope", "pq_kv_row_bytes", "pq_kv_append", "pq_kv_load",
+           "pq_attn_decode_workspace_bytes", "pq_attn_decode")
 
 
 class PQError(RuntimeError):
@@ -66,6 +68,21 @@ class pq_step_mat(ctypes.Structure):
                 ("v_alpha", ctypes.c_void_p), ("wq_bf16", ctypes.c_void_p), ("codes", ctypes.c_void_p),
                 ("dalpha", ctypes.c_void_p), ("grad_scale", ctypes.c_double), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64)]
+
+
+class pq_rope_scaling(ctypes.Structure):
+    """Mirror of `struct pq_rope_scaling` in include/pq.h."""
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("trained", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class pq_kv_cache(ctypes.Structure):
+    """Mirror of `struct pq_kv_cache` in include/pq.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_param", ctypes.c_void_p),
+                ("v_param", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -105,8 +122,19 @@ def _load():
     L.pq_pack_grouped.argtypes = [i32, i32, vp, vp, vp]
     L.pq_qat_step.argtypes = [i32, i64, i64, vp, vp, vp, i32, dbl, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.pq_qat_step_grouped.argtypes = [i32, i32, vp, vp, i32, vp, vp]
+    L.pq_rope_table.argtypes = [i64, i64, dbl, vp, vp, vp]
+    L.pq_rope.argtypes = [i32, i64, i64, i64, i64, i32, i32, vp, i64, i64, vp, vp, i64, vp, i64, i64, vp]
+    L.pq_kv_row_bytes.argtypes = [i32, i64]
+    L.pq_kv_row_bytes.restype = i64
+    L.pq_kv_append.argtypes = [vp, i32, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, i64, i64, i32,
+                               vp, i64, i64, i64, vp, i64, i64, vp]
+    L.pq_kv_load.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, vp, vp, i64, i64, vp, i64, i64, vp]
+    L.pq_attn_decode_workspace_bytes.argtypes = [vp, i64, i64]
+    L.pq_attn_decode_workspace_bytes.restype = i64
+    L.pq_attn_decode.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, i64, i64, vp, dbl, i64, i64, vp, i64, i64,
+                                 vp, vp, i64, vp]
     for name in EXPORTS:
-        if name not in ("pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_status_str",
+        if name not in ("pq_kv_row_bytes", "pq_attn_decode_workspace_bytes", "pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_status_str",
                         "pq_version", "pq_num_levels", "pq_gemm_workspace_bytes"):
             getattr(L, name).restype = i32
     return L
@@ -339,3 +367,204 @@ def pq_qat_step(mode, rows, cols, W, alpha, G, g_dtype, grad_scale, mW, vW, m_al
 def pq_qat_step_grouped(mode, table: StepTable, hp: pq_adamw, g_dtype=PQ_G_F32, stream=None) -> None:
     _check(lib.pq_qat_step_grouped(mode, table.count, table.host_ptr, table.dev_ptr, g_dtype,
                                    ctypes.addressof(hp), _stream(stream)), "pq_qat_step_grouped")
+
+
+# ------------------------------------------------------------------ serving
+# Rotary positions, the key-value cache and attention over it.  Sizes and
+# strides come from the tensors; everything else is checked by the library.
+
+PQ_F32, PQ_BF16, PQ_F16 = 0, 1, 2
+PQ_ROPE_HALF, PQ_ROPE_INTERLEAVED = 0, 1
+PQ_ROPE_PLAIN, PQ_ROPE_LINEAR, PQ_ROPE_NTK, PQ_ROPE_YARN, PQ_ROPE_BANDS = 0, 1, 2, 3, 4
+PQ_KV_16, PQ_KV_8, PQ_KV_4 = 0, 1, 2
+_DTYPE = {torch.float32: PQ_F32, torch.bfloat16: PQ_BF16, torch.float16: PQ_F16}
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what}: {t.dtype} is none of float32, bfloat16, float16") from None
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(token stride, head stride) in elements of t [tokens, heads, dim]."""
+    _want(t.dim() == 3, f"{what}: [tokens, heads, dim] wanted")
+    a, b, c = t.stride()
+    _want(c == 1 or t.shape[2] == 1, f"{what}: the last dimension has to be contiguous")
+    return a, b
+
+
+def _array(t: torch.Tensor, dtype: torch.dtype, n: int, what: str) -> int:
+    """The address of a contiguous index array of n elements."""
+    _want(t.dtype == dtype and t.numel() == n and t.is_contiguous(), f"{what}: {n} contiguous {dtype} wanted")
+    return t.data_ptr()
+
+
+def pq_rope_table(max_pos, rot, base=10000.0, table=None, scaling: Optional[pq_rope_scaling] = None, stream=None,
+                  device="cuda") -> torch.Tensor:
+    """The (cos, sin) rows of positions 0 .. max_pos - 1: f32 [max_pos, rot / 2, 2], made here if not given."""
+    if table is None:
+        table = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device)
+        if stream is not None:
+            table.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    _check(lib.pq_rope_table(max_pos, rot, float(base), ctypes.addressof(scaling) if scaling is not None else None,
+                             _array(table, torch.float32, max_pos * rot, "table"), _stream(stream)), "pq_rope_table")
+    return table
+
+
+def rope_scaling(kind, factor, trained=0.0, beta_fast=None, beta_slow=1.0) -> pq_rope_scaling:
+    """A scaling of pq_rope_table; beta_fast defaults to the kind's usual value."""
+    if beta_fast is None:
+        beta_fast = 4.0 if kind == PQ_ROPE_BANDS else 32.0
+    return pq_rope_scaling(int(kind), 0, float(factor), float(trained), float(beta_fast), float(beta_slow))
+
+
+def _table_shape(table: torch.Tensor):
+    _want(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2 and table.is_contiguous(),
+          "table: contiguous float32 [max_pos, rot / 2, 2] wanted")
+    return table.shape[0], 2 * table.shape[1]
+
+
+def pq_rope(x, positions, table, y=None, layout=PQ_ROPE_HALF, inverse=False, stream=None) -> None:
+    """Rotate x [tokens, heads, dim] into y (None: in place); inverse=True is the gradient's rotation."""
+    y = x if y is None else y
+    _want(y.shape == x.shape and y.dtype == x.dtype, "y: the shape and type of x wanted")
+    xt, xh = _rows(x, "x")
+    yt, yh = _rows(y, "y")
+    n, heads, dim = x.shape
+    max_pos, rot = _table_shape(table)
+    _check(lib.pq_rope(_dtype(x, "x"), n, heads, dim, rot, layout, 1 if inverse else 0, x.data_ptr(), xt, xh,
+                       _array(positions, torch.int32, n, "positions"), table.data_ptr(), max_pos, y.data_ptr(), yt, yh,
+                       _stream(stream)), "pq_rope")
+
+
+def pq_kv_row_bytes(fmt: int, dim: int) -> int:
+    return int(lib.pq_kv_row_bytes(fmt, dim))
+
+
+class KVCache:
+    """A paged key-value cache: the caller's arrays and their pq_kv_cache.
+
+    k and v are [pages, heads, page_size, row] views with equal strides --
+    transpose(1, 2) of [pages, page_size, heads, row] arrays for token-major
+    pages -- in bf16 or f16 (PQ_KV_16, row = dim) or uint8 (PQ_KV_8, row =
+    dim; PQ_KV_4, row = dim / 2); k_param and v_param are contiguous bf16
+    [pages, heads, page_size, 2]."""
+
+    def __init__(self, fmt, page_size, k, v, k_param=None, v_param=None):
+        _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype,
+              "k, v: [pages, heads, page_size, row] of one type, shape and strides wanted")
+        pages, heads, tokens, row = k.shape
+        _want(tokens == page_size and k.stride(3) == 1, "k, v: page_size tokens of contiguous rows wanted")
+        _want(fmt in (PQ_KV_16, PQ_KV_8, PQ_KV_4), "fmt: PQ_KV_16, PQ_KV_8 or PQ_KV_4 wanted")
+        if fmt == PQ_KV_16:
+            _want(k.dtype in (torch.bfloat16, torch.float16), "k, v: bfloat16 or float16 wanted")
+            dim, dtype = row, _DTYPE[k.dtype]
+        else:
+            _want(k.dtype == torch.uint8, "k, v: uint8 wanted")
+            dim, dtype = row * (1 if fmt == PQ_KV_8 else 2), 0
+            for p in (k_param, v_param):
+                _want(p is not None and p.dtype == torch.bfloat16 and tuple(p.shape) == (pages, heads, tokens, 2) and
+                      p.is_contiguous(), "k_param, v_param: contiguous bfloat16 [pages, heads, page_size, 2] wanted")
+        self.tensors = (k, v, k_param, v_param)          # kept alive with the addresses
+        self.format, self.page_size, self.heads, self.dim, self.num_pages = fmt, page_size, heads, dim, pages
+        size = k.element_size()
+        s = [x * size for x in k.stride()[:3]]
+        self.struct = pq_kv_cache(k.data_ptr(), v.data_ptr(), _ptr(k_param), _ptr(v_param), pages, s[0], s[1], s[2],
+                                  fmt, dtype, page_size, heads, dim, 0)
+        self.ptr = ctypes.addressof(self.struct)
+
+    @classmethod
+    def allocate(cls, fmt, num_pages, page_size, heads, dim, dtype=torch.bfloat16, device="cuda"):
+        """A zeroed cache with head-major pages."""
+        row = dim if fmt != PQ_KV_4 else dim // 2
+        shape = (num_pages, heads, page_size)
+        kind = dtype if fmt == PQ_KV_16 else torch.uint8
+        k, v = (torch.zeros(*shape, row, dtype=kind, device=device) for _ in range(2))
+        if fmt == PQ_KV_16:
+            return cls(fmt, page_size, k, v)
+        return cls(fmt, page_size, k, v, *(torch.zeros(*shape, 2, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+
+def pq_kv_append(cache: KVCache, k, v, slots, positions=None, table=None, layout=PQ_ROPE_HALF, q=None, q_out=None,
+                 stream=None) -> None:
+    """Write k, v [tokens, heads, dim] into the cache at slots; with a table k is rotated on the way, and q
+    [tokens, q_heads, dim] is rotated into q_out (None: in place) in the same launch."""
+    n = k.shape[0]
+    kt, kh = _rows(k, "k")
+    vt, vh = _rows(v, "v")
+    _want(k.shape == v.shape and k.dtype == v.dtype and tuple(k.shape[1:]) == (cache.heads, cache.dim),
+          "k, v: [tokens, heads, dim] of the cache and one type wanted")
+    max_pos, rot, pp, tp = 0, 0, None, None
+    if table is not None:
+        max_pos, rot = _table_shape(table)
+        tp = table.data_ptr()
+        pp = None if positions is None else _array(positions, torch.int32, n, "positions")
+    qh, qp, qop, qs, qos = 0, None, None, (0, 0), (0, 0)
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        qs, qos = _rows(q, "q"), _rows(q_out, "q_out")
+        _want(q_out.shape == q.shape and q.shape[0] == n and q.shape[2] == cache.dim and q.dtype == k.dtype and
+              q_out.dtype == k.dtype, "q, q_out: [tokens, q_heads, dim] of k's type wanted")
+        qh, qp, qop = q.shape[1], q.data_ptr(), q_out.data_ptr()
+    _check(lib.pq_kv_append(cache.ptr, _dtype(k, "k"), n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                            _array(slots, torch.int64, n, "slots"), pp, tp, max_pos, rot, layout, qp, qh, qs[0], qs[1],
+                            qop, qos[0], qos[1], _stream(stream)), "pq_kv_append")
+
+
+def _block_table(block_table, batch: int):
+    _want(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == batch and
+          (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [batch, pages] wanted")
+    return block_table.data_ptr(), block_table.stride(0), block_table.shape[1]
+
+
+def pq_kv_load(cache: KVCache, block_table, starts, cu, k_out, v_out, stream=None) -> None:
+    """Read tokens starts[b] .. of each sequence into rows cu[b] .. cu[b + 1] of k_out and v_out."""
+    batch = cu.numel() - 1
+    bp, bs, bn = _block_table(block_table, batch)
+    _want(k_out.shape == v_out.shape and k_out.dtype == v_out.dtype and
+          tuple(k_out.shape[1:]) == (cache.heads, cache.dim), "k_out, v_out: [tokens, heads, dim] of one type wanted")
+    kt, kh = _rows(k_out, "k_out")
+    vt, vh = _rows(v_out, "v_out")
+    _check(lib.pq_kv_load(cache.ptr, _dtype(k_out, "k_out"), batch, k_out.shape[0], bp, bs, bn,
+                          None if starts is None else _array(starts, torch.int32, batch, "starts"),
+                          _array(cu, torch.int32, batch + 1, "cu"), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh,
+                          _stream(stream)), "pq_kv_load")
+
+
+def pq_attn_decode_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> int:
+    return int(lib.pq_attn_decode_workspace_bytes(cache.ptr, batch, q_heads))
+
+
+def attn_workspace(cache: KVCache, batch: int, q_heads: int, device="cuda") -> torch.Tensor:
+    """A workspace for pq_attn_decode calls of this size, for the caller to keep."""
+    n = pq_attn_decode_workspace_bytes(cache, batch, q_heads)
+    if n < 0:
+        raise PQError(2, "pq_attn_decode_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def pq_attn_decode(cache: KVCache, q, block_table, lens, out, lse=None, scale=None, window=0, max_len=0,
+                   workspace=None, stream=None) -> None:
+    """Attention of one new token per sequence, q [batch, q_heads, dim], over the cache; scale defaults to
+    1 / sqrt(dim).  Without a workspace one is allocated for the call."""
+    batch, q_heads, dim = q.shape
+    _want(dim == cache.dim and out.shape == q.shape and out.dtype == q.dtype, "q, out: [batch, q_heads, dim] wanted")
+    qs, os_ = _rows(q, "q"), _rows(out, "out")
+    bp, bs, bn = _block_table(block_table, batch)
+    if workspace is None:
+        workspace = attn_workspace(cache, batch, q_heads, q.device)
+        if stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    _check(lib.pq_attn_decode(cache.ptr, _dtype(q, "q"), batch, q_heads, q.data_ptr(), qs[0], qs[1], bp, bs, bn,
+                              _array(lens, torch.int32, batch, "lens"), dim ** -0.5 if scale is None else float(scale),
+                              window, max_len, out.data_ptr(), os_[0], os_[1],
+                              None if lse is None else _array(lse, torch.float32, batch * q_heads, "lse"),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "pq_attn_decode")

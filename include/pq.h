@@ -520,6 +520,194 @@ pq_status pq_quantize_fwd_stats(int mode, int64_t rows, int64_t cols, const floa
 pq_status pq_weight_movement(int64_t rows, int64_t cols, const float *W, const float *W0,
                              double *sq_diff, double *sq_ref, void *stream);
 
+/*
+ * Serving: rotary positions, a key-value cache held in 16, 8 or 4 bits, and
+ * attention of one new token over it -- what a decode step needs between the
+ * packed-weight GEMMs.  The conventions at the top of this file hold, with
+ * these additions: activations may be strided (strides in elements, the last
+ * dimension contiguous); a NULL stream is the null stream; sizes of zero
+ * enqueue nothing.
+ */
+
+/* Element types of activations (PQ_G_F32 and PQ_G_BF16 have the same values). */
+#define PQ_F32 0
+#define PQ_BF16 1
+#define PQ_F16 2
+
+/* Pairs of a head's first `rot` channels that are rotated together:
+ * PQ_ROPE_HALF (c, c + rot / 2); PQ_ROPE_INTERLEAVED (2c, 2c + 1). */
+#define PQ_ROPE_HALF 0
+#define PQ_ROPE_INTERLEAVED 1
+
+/* How pq_rope_table scales the angles for contexts longer than the trained
+ * one.  With f_c = base^(-2c / rot) and s = factor:
+ *   PQ_ROPE_PLAIN   f_c
+ *   PQ_ROPE_LINEAR  f_c / s
+ *   PQ_ROPE_NTK     base replaced by base * s^(rot / (rot - 2)); rot > 2
+ *   PQ_ROPE_YARN    f_c ((1 - g) / s + g), g = 1 - clamp((c - lo) / (hi - lo), 0, 1)
+ *                   with lo, hi the (rounded outwards, clamped to [0, rot - 1])
+ *                   pair indices that make `beta_fast` and `beta_slow` turns in
+ *                   `trained` positions; cos and sin are also multiplied by
+ *                   0.1 ln s + 1
+ *   PQ_ROPE_BANDS   wavelength w = 2 pi / f_c: f_c / s where w > trained / beta_slow,
+ *                   f_c where w < trained / beta_fast, in between
+ *                   f_c ((1 - g) / s + g), g = (trained / w - beta_slow) / (beta_fast - beta_slow)
+ */
+#define PQ_ROPE_PLAIN 0
+#define PQ_ROPE_LINEAR 1
+#define PQ_ROPE_NTK 2
+#define PQ_ROPE_YARN 3
+#define PQ_ROPE_BANDS 4
+
+typedef struct pq_rope_scaling {
+    int32_t kind;         /* PQ_ROPE_PLAIN ..                               */
+    int32_t reserved;     /* 0                                              */
+    double factor;        /* s >= 1                                         */
+    double trained;       /* YARN, BANDS: trained context length, > 0       */
+    double beta_fast;     /* YARN: 32; BANDS: 4 (> beta_slow)               */
+    double beta_slow;     /* YARN, BANDS: 1 (> 0)                           */
+} pq_rope_scaling;
+
+/* pq_rope_table -- the (cos, sin) rows of positions 0 .. max_pos - 1, made
+ * once per model: table [max_pos, rot / 2, 2] fp32, each value rounded once
+ * from binary64.
+ *   rot      even, 2 .. 1024;  max_pos 0 .. 2^31 - 1;  base > 1
+ *   scaling  host pointer read during the call, or NULL for PQ_ROPE_PLAIN
+ * An unknown kind -> PQ_ERR_MODE; base or a scaling value out of range (or
+ * not finite) -> PQ_ERR_ARG. */
+pq_status pq_rope_table(int64_t max_pos, int64_t rot, double base, const pq_rope_scaling *scaling,
+                        float *table, void *stream);
+
+/* pq_rope -- rotary positions of x [tokens, heads, dim]: each pair (x1, x2)
+ * of the first `rot` channels becomes
+ *   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * in fp32 (one rounding an operation), rounded once to the type; the other
+ * channels are copied.  `inverse` != 0 takes -sin: the transposed rotation,
+ * which is the gradient of the forward call.
+ *   dtype      PQ_F32, PQ_BF16 or PQ_F16, of x and y
+ *   dim        1 .. 1024;  rot even, 0 .. dim
+ *   strides    elements between tokens and between heads, any value
+ *   positions  in [tokens] int32.  A negative one (padding) leaves the row as
+ *              it is; one past the table gives NaN in the rotated channels
+ *   table      in [max_pos, rot / 2, 2] of pq_rope_table (or any cos, sin)
+ *   y          out; y == x with equal strides works in place, any other
+ *              overlap is not allowed
+ * Only the element alignment of x and y is required (else PQ_ERR_ALIGN). */
+pq_status pq_rope(int dtype, int64_t tokens, int64_t heads, int64_t dim, int64_t rot, int layout, int inverse,
+                  const void *x, int64_t x_token_stride, int64_t x_head_stride, const int32_t *positions,
+                  const float *table, int64_t max_pos, void *y, int64_t y_token_stride, int64_t y_head_stride,
+                  void *stream);
+
+/* Formats of a key-value cache.  PQ_KV_16: the values themselves (bf16 or
+ * f16).  PQ_KV_8, PQ_KV_4: a row (the `dim` channels of one token and head, K
+ * and V apart) is held as unsigned codes n in 0 .. Q (Q = 255, 15) and one
+ * pair of bf16, a scale s and a zero z:  x^ = z + s n  with
+ *   z = bf16(min x),  s = max(bf16((max x - min x) fl32(1 / Q)), 2^-60),
+ *   n = clamp(rint((x - z) r), 0, Q),  r = fl32(1 / s),
+ * fp32 throughout, one rounding an operation, rint to even.  A row that holds
+ * a NaN is stored with a NaN zero and reads back as NaN. */
+#define PQ_KV_16 0
+#define PQ_KV_8 1
+#define PQ_KV_4 2
+
+/* A paged cache: page p, head h, token t of the page at
+ *   k + p * page_stride + h * head_stride + t * token_stride  (bytes)
+ * so that head-major and token-major pages, and K and V in one array, are
+ * all described by strides.  A row is pq_kv_row_bytes(format, dim) contiguous
+ * bytes; 4-bit rows hold channel 2i in the low half of byte i. */
+typedef struct pq_kv_cache {
+    void *k, *v;              /* 16-byte aligned                            */
+    void *k_param, *v_param;  /* PQ_KV_8, PQ_KV_4: bf16 pairs (s, z),
+                                 [num_pages, heads, page_size, 2]; 16 bit: NULL */
+    int64_t num_pages;
+    int64_t page_stride, head_stride, token_stride;   /* bytes, >= 0, multiples of 8 */
+    int32_t format;           /* PQ_KV_16, PQ_KV_8, PQ_KV_4                 */
+    int32_t dtype;            /* PQ_KV_16: PQ_BF16 or PQ_F16                */
+    int32_t page_size;        /* tokens: a power of two, 16 .. 32768        */
+    int32_t heads;            /* 1 .. 65535                                 */
+    int32_t dim;              /* a multiple of 16, 16 .. 256                */
+    int32_t reserved;         /* 0                                          */
+} pq_kv_cache;
+
+/* Bytes of a row (2, 1 or 1/2 per channel), -1 for a bad format or dim. */
+int64_t pq_kv_row_bytes(int format, int64_t dim);
+
+/*
+ * pq_kv_append -- write new tokens' keys and values into the cache, rotating
+ * the keys (and the queries) on the way.
+ *   cache      host pointer read during the call
+ *   dtype      of k, v, q and q_out: PQ_F32, PQ_BF16 or PQ_F16
+ *   k, v       in [tokens, heads, dim], strides in elements
+ *   slots      in [tokens] int64: page * page_size + offset.  A slot below 0
+ *              or past the cache is skipped (padding).  Two tokens with the
+ *              same slot: either may stay
+ *   table      (with positions, max_pos, rot, layout, as pq_rope) rotates k
+ *              in fp32 before it is stored, so that it is rounded once; NULL
+ *              stores k as it is
+ *   q, q_out   [tokens, q_heads, dim]: rotated into q_out in the same launch
+ *              (q_out == q in place); NULL with q_heads 0 for none; a q
+ *              without a table -> PQ_ERR_ARG
+ * k, v, q and q_out 16-byte aligned, their strides multiples of 8 elements.
+ */
+pq_status pq_kv_append(const pq_kv_cache *cache, int dtype, int64_t tokens, const void *k, int64_t k_token_stride,
+                       int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                       const int64_t *slots, const int32_t *positions, const float *table, int64_t max_pos,
+                       int64_t rot, int layout, const void *q, int64_t q_heads, int64_t q_token_stride,
+                       int64_t q_head_stride, void *q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                       void *stream);
+
+/*
+ * pq_kv_load -- read tokens back into dense arrays.  Output row i, with
+ * cu[b] <= i < cu[b + 1], is token starts[b] + i - cu[b] of sequence b, whose
+ * page j is block_table[b * table_stride + j].
+ *   dtype        of k_out and v_out (x^ in fp32, rounded once)
+ *   starts       in [batch] int32, or NULL for 0
+ *   cu           in [batch + 1] int32, not decreasing, cu[0] = 0
+ *   tokens       rows of k_out and v_out (cu[batch], known to the caller)
+ *   max_pages    columns of block_table.  A token past them, a page id outside
+ *                the cache and rows past cu[batch] read as 0
+ *   k_out, v_out out [tokens, heads, dim], 16-byte aligned, strides (in
+ *                elements) multiples of 8
+ */
+pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t tokens, const int32_t *block_table,
+                     int64_t table_stride, int64_t max_pages, const int32_t *starts, const int32_t *cu, void *k_out,
+                     int64_t ko_token_stride, int64_t ko_head_stride, void *v_out, int64_t vo_token_stride,
+                     int64_t vo_head_stride, void *stream);
+
+/*
+ * pq_attn_decode -- attention of one new token per sequence over the cache:
+ *   x_t = scale * q . k^_t,   t in [max(0, len - window), len)
+ *   out = sum_t softmax(x)_t v^_t,   lse = ln sum_t exp x_t
+ * in fp32; query head h reads cache head h / (q_heads / heads).
+ *   q, out       [batch, q_heads, dim] of q_dtype (PQ_BF16 or PQ_F16; the
+ *                cache's dtype if that is PQ_KV_16), 16-byte aligned, strides
+ *                (elements) multiples of 8
+ *   q_heads      a positive multiple of cache->heads
+ *   block_table  in [batch, max_pages] int32 with rows table_stride apart.
+ *                Only the entries of attended tokens are used; a page id
+ *                outside the cache hides its tokens
+ *   lens         in [batch] int32: tokens in the cache, the new one among
+ *                them, clamped to [0, max_pages * page_size].  Nothing to
+ *                attend to gives out = 0 and lse = -inf; what lies in the
+ *                cache past len or before the window is never used, NaN and
+ *                infinities included
+ *   window       attended tokens, 0 for all of them
+ *   max_len      an upper bound of lens that sizes the launch (0: max_pages *
+ *                page_size); the result for longer sequences is still right
+ *   lse          out [batch, q_heads] fp32, or NULL
+ *   workspace    device memory of pq_attn_decode_workspace_bytes(cache,
+ *                batch, q_heads) bytes, 16-byte aligned
+ * For fixed arguments the result is the same in every run (max_len and the
+ * other sequences of a batch decide where a sequence is split, and with it
+ * the order of its sums).
+ */
+int64_t pq_attn_decode_workspace_bytes(const pq_kv_cache *cache, int64_t batch, int64_t q_heads);
+pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, int64_t q_heads, const void *q,
+                         int64_t q_batch_stride, int64_t q_head_stride, const int32_t *block_table,
+                         int64_t table_stride, int64_t max_pages, const int32_t *lens, double scale, int64_t window,
+                         int64_t max_len, void *out, int64_t out_batch_stride, int64_t out_head_stride, float *lse,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
