@@ -7,27 +7,37 @@
 //   p_t = 2^(x_t - m),  l = sum p_t,  o = sum p_t v^_t,  out = o / l,
 // and whenever m grows by d, l and o are multiplied by 2^-d.
 //
-// Affine rows k^ = z + s n leave the products as scalars of a token,
-//   q . k^ = s (q . n) + z sum q,      sum p v^ = sum (p s) n + sum p z,
+// Affine rows k^ = z + s n leave the products as scalars of a token; with the
+// middle code c,
+//   q . k^ = s (q . (n - c)) + (z + s c) sum q,
+//   sum p v^ = sum (p s) n + sum p z,
 // so the matrix unit works on the bare codes: a code byte, zero-extended to
 // 16 bits, is the f16 subnormal n 2^-24, which the f16 MFMA multiplies
-// exactly.  One byte permute places two codes; nothing is converted.
+// exactly.  One byte permute places two codes; nothing is converted.  The
+// first product starts from -c sum q, so that only the small difference is
+// rounded afterwards.
 //
-// Layout.  A wave takes 32 tokens at a time.  S^T = K Q^T (rows: tokens,
-// columns: the heads of a group, up to 16) leaves lane (head = lane % 16,
-// kb = lane / 16) with the scores of tokens 4 kb + i of two 16-token tiles.
-// Those eight are, in that order, the k-index run 8 kb .. 8 kb + 7 of the
-// second product O^T = V^T P^T, for any order of tokens that P and V share:
-// the probabilities go from accumulator to operand in their own registers.
-// V^T needs eight tokens of one channel per lane; a lane loads 16 / 8 / 4-bit
+// Layout.  S^T = K Q^T (rows: 16 tokens, columns: 16 heads) leaves lane
+// (column = lane % 16, kb = lane / 16) with the scores of tokens 4 kb + i.
+// Those of two tiles are, in that order, the k-index run 8 kb .. 8 kb + 7 of
+// the second product O^T = V^T P^T, for any order of tokens that P and V
+// share: the probabilities go from accumulator to operand in their own
+// registers.  V^T needs eight tokens of one channel per lane; a lane loads
 // runs of the same channels of its eight tokens and transposes them with byte
 // permutes.  No LDS and no cross-lane traffic in the loop but a maximum.
 //
+// Groups of few heads would leave most columns, and with them most lanes of
+// the softmax, without work.  With R = 2 the columns hold R copies of
+// the group's heads; a wave takes R blocks of 32 tokens at a time and copy r
+// of the columns keeps block r only (its own m, l and o), so that every lane
+// works on tokens of its own: the softmax costs 1 / R.
+//
 // Work split.  The cache is read once and every byte costs the same, so the
-// 128-token tiles of all (sequence, head) rows are laid end to end and cut
-// into equal shares, one per block, whatever the lengths are.  A row that lies
-// in one share is written directly; the others leave (m, l, o) per share in
-// the workspace and a second kernel joins them in order.
+// steps of all (sequence, head) rows are laid end to end and cut into equal
+// shares, one per block, whatever the lengths are.  A row that lies in one
+// share is written directly; of the others each share leaves (m, l, o) in the
+// workspace, and a second kernel joins them, in order.  Short rows are not
+// split: one block each and no second kernel.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -42,9 +52,11 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 128;          // tokens of a scheduling unit: 32 per wave
-constexpr int kMaxBatch = 1024;     // sequences of one launch (their tile counts sit in LDS)
-constexpr int kMaxShares = 512;     // blocks of one launch
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kMaxBatch = 1024;     // sequences of one launch (their step counts sit in LDS)
+constexpr int kMaxShares = 512;     // blocks of one launch: two per CU
+constexpr int kWaves = 4;
 
 struct AttnArgs {
     const uint8_t *k, *v;
@@ -55,19 +67,20 @@ struct AttnArgs {
     int64_t q_bs, q_hs;
     const int32_t *table;
     int64_t table_stride;
-    int64_t max_tokens;             // max_pages * page_size
+    int max_tokens;                 // most that max_pages and max_len allow, at most 2^30
     const int32_t *lens;
     int batch, group, gtiles;       // query heads per cache head; 16-head tiles of a group
     int group_rows;                 // rows of a partial: min(group, 16)
-    int64_t window;
+    int window;                     // 0: everything
     float scale_log2;               // scale * log2(e)
     uint16_t *out;
     int64_t out_bs, out_hs;
     float *lse;
     int q_heads;
-    float *part_o;                  // [2 shares][group_rows][dim]
-    float *part_ml;                 // [2 shares][group_rows][2]
-    int shares;
+    float *part_o;                  // [2 kMaxShares][group_rows][dim]
+    f32x2 *part_ml;                 // [2 kMaxShares][group_rows] (m, l)
+    int2 *spans;                    // [batch][heads][gtiles]: a row's first partial and last share
+    int shares;                     // 0: one block per row
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -75,62 +88,73 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // Attended range of a sequence, its first token rounded down to a 16-token
 // tile: pages are whole numbers of those.
 struct Range {
-    int64_t first, len, base;       // base = first & ~15
-    __device__ __forceinline__ int64_t tiles() const { return len > first ? (len - base + kTile - 1) / kTile : 0; }
+    int first, len, base;           // base = first & ~15
+    __device__ __forceinline__ int steps(int unit) const { return len > first ? (len - base + unit - 1) / unit : 0; }
 };
 
-__device__ __forceinline__ Range range_of(const AttnArgs &a, int b)
+__device__ __forceinline__ Range range_of(const AttnArgs &a, int len)
 {
     Range r;
-    int64_t n = a.lens[b];
-    n = n < 0 ? 0 : n;
-    r.len = n < a.max_tokens ? n : a.max_tokens;
+    r.len = min(max(len, 0), a.max_tokens);
     r.first = a.window > 0 && r.len > a.window ? r.len - a.window : 0;
-    r.base = r.first & ~static_cast<int64_t>(15);
+    r.base = r.first & ~15;
     return r;
 }
 
-// pre[i] = tiles of sequences before i, pre[batch] their sum; 256 threads.
-__device__ __forceinline__ void tile_prefix(const AttnArgs &a, int64_t *pre, int64_t *wave_sum)
+// lens[i] = clamped lengths; pre[i] = steps of sequences before i, pre[batch]
+// their sum; 256 threads.
+__device__ __forceinline__ void step_prefix(const AttnArgs &a, int unit, int *lens, int *pre, int *wave_sum)
 {
-    int64_t before = 0;
+    int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 256) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        const int64_t n = b < a.batch ? range_of(a, b).tiles() : 0;
-        int64_t s = n;
+        const Range r = range_of(a, b < a.batch ? a.lens[b] : 0);
+        const int n = r.steps(unit);
+        int s = n;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const int64_t up = __shfl_up(s, o);
+            const int up = __shfl_up(s, o);
             if ((threadIdx.x & 63) >= static_cast<unsigned>(o)) s += up;
         }
         if ((threadIdx.x & 63) == 63) wave_sum[threadIdx.x >> 6] = s;
         __syncthreads();
-        int64_t at = before;
-        for (int w = 0; w < 4; ++w) {
+        int at = before;
+        for (int w = 0; w < kWaves; ++w) {
             if (w < static_cast<int>(threadIdx.x >> 6)) at += wave_sum[w];
             before += wave_sum[w];
         }
-        if (b < a.batch) pre[b] = at + s - n;
+        if (b < a.batch) {
+            pre[b] = at + s - n;
+            lens[b] = r.len;
+        }
         __syncthreads();
     }
     if (threadIdx.x == 0) pre[a.batch] = before;
     __syncthreads();
 }
 
-// Which partial a share writes for a row whose first tile is `row0`: the one
-// for the row it starts inside (or at), or the one for the row it ends in.
-__device__ __forceinline__ int64_t part_slot(int64_t share, int64_t row0, int64_t per_share)
-{
-    return 2 * share + (row0 > share * per_share ? 1 : 0);
-}
+// The cut into shares: the first `more` shares have `each` + 1 steps, the
+// others `each`.
+struct Cut {
+    int each, more;
+    __device__ __forceinline__ int begin(int share) const { return share * each + min(share, more); }
+    __device__ __forceinline__ int share_of(int step) const
+    {
+        const int wide = more * (each + 1);
+        return step < wide ? step / (each + 1) : more + (step - wide) / each;
+    }
+    // Which partial a share writes for the row that starts at step `row0`:
+    // that of the row it begins in, or that of the row it ends in.
+    __device__ __forceinline__ int slot(int share, int row0) const { return 2 * share + (row0 > begin(share) ? 1 : 0); }
+};
 
-// max / sum over the lanes that hold the same head (lane % 16).
-__device__ __forceinline__ float head_max(float x)
+// max / sum over the lanes of a column (lane % 16).
+__device__ __forceinline__ float column_max(float x)
 {
     x = fmaxf(x, __shfl_xor(x, 16));
     return fmaxf(x, __shfl_xor(x, 32));
 }
-__device__ __forceinline__ float head_sum(float x)
+__device__ __forceinline__ float column_sum(float x)
 {
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
@@ -146,60 +170,77 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 }
 
 // QT: type of q and out (and of a 16-bit cache).  FMT: cache format.  DP: dim
-// rounded up to 64, 128 or 256.
-template <typename QT, int FMT, int DP>
+// rounded up to 64, 128 or 256.  R: copies of the heads in the columns.
+template <typename QT, int FMT, int DP, int R>
 struct Attn {
     static constexpr bool kRaw = FMT == PQ_KV_16;
     static constexpr bool kF16 = !kRaw || __is_same(QT, f16_t);   // operand type of both products
     using OT = typename std::conditional<kF16, f16_t, bf16_t>::type;
+    // The weights p (or p s) enter the second product as two 16-bit values,
+    // the second carrying the first one's remainder: rounded to one (2^-9
+    // off in bf16, 2^-12 in f16) they would add as much to the output's error
+    // as its own rounding.  The matrix unit has the room.
+    static constexpr int kUnit = 32 * R;    // tokens of a step
+    static constexpr int kCols = 16 / R;    // heads of a tile
     static constexpr int KS = DP / 32;      // k steps of the first product
     static constexpr int E = DP / 16;       // channels of a lane in the second
-    // Operand order of the channels of step s in lane group kb.  16-bit rows:
-    // 32 s + 8 kb + j.  Codes: steps 2c, 2c + 1 share the 16-channel run
-    // 64 c + 16 kb (16 or 8 bytes, one load).
-    // The probabilities are scaled by 2^kShift, so that an f16 keeps 24 bits
-    // of range below the largest before it becomes subnormal.
-    static constexpr float kShift = kF16 ? 7.f : 0.f;
-    static constexpr float kSlack = 8.f;    // m may lag behind the maximum by this much
+    // Words of a lane per 16 tokens: K in KC runs of KW words (16-bit rows: 8
+    // channels of step s at 32 s + 8 kb; codes: 16 channels at 64 c + 16 kb,
+    // which are steps 2c and 2c + 1), V in VW words per token.
+    static constexpr int KC = kRaw ? KS : KS / 2, KW = FMT == PQ_KV_4 ? 2 : 4;
+    static constexpr int VW = kRaw ? E / 2 : FMT == PQ_KV_8 ? E / 4 : E >= 8 ? E / 8 : 1;
+    // The weights are scaled by 2^kShift, so that an f16 keeps 22 octaves
+    // below the largest before it becomes subnormal; m may lag behind the
+    // maximum by kSlack, so that it seldom moves.
+    static constexpr float kShift = kF16 ? 7.f : 0.f, kSlack = 8.f;
 
     u32x4 q[KS];
     f32x4 o[E];
     float m, l, zsum;
-    float c1, c2;                   // x = s_k (acc c1) + z_k c2   (raw: x = acc c1)
+    float c1, c2;                   // x = s_k (acc c1) + (z_k + s_k c) c2   (16-bit rows: x = acc c1)
+    f32x4 acc0;                     // start of the first product
+    uint32_t k[R][2][KC][KW], v[R][2][4][VW];   // two 16-token tiles per block; V: tokens 4 kb + j
+    u32x4 kpar[2], vpar[2];         // pairs of tokens 4 kb + i of the lane's own block
 
+    static __device__ __forceinline__ int column() { return threadIdx.x & 15; }
+    static __device__ __forceinline__ int kb() { return (threadIdx.x & 63) >> 4; }
+    static __device__ __forceinline__ int copy() { return column() / kCols; }
+
+    // The heads' channels as they lie in memory (set_q turns them into operands).
     __device__ __forceinline__ void load_q(const AttnArgs &a, int b, int kvh, int gt)
     {
-        const int lane = threadIdx.x & 63, head = lane & 15, kb = lane >> 4;
-        const int g = gt * 16 + head;
+        const int g = gt * 16 + column() % kCols;
         const bool on = g < a.group;
         const uint16_t *row = a.q + b * a.q_bs + static_cast<int64_t>(kvh * a.group + (on ? g : 0)) * a.q_hs;
-        float f[KS][8];
-        float amax = 0.f, sum = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int d = kRaw ? 32 * s + 8 * kb : 64 * (s >> 1) + 16 * kb + 8 * (s & 1);
-            u32x4 w = {0, 0, 0, 0};
-            if (on && d < a.dim) w = *reinterpret_cast<const u32x4 *>(row + d);
-            if constexpr (kRaw) {
-                q[s] = w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) unpack16<QT>(w[e], f[s][2 * e], f[s][2 * e + 1]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    amax = fmaxf(amax, fabsf(f[s][e]));
-                    sum += f[s][e];
-                }
-            }
+            const int d = kRaw ? 32 * s + 8 * kb() : 64 * (s >> 1) + 16 * kb() + 8 * (s & 1);
+            q[s] = u32x4{0, 0, 0, 0};
+            if (on && d < a.dim) q[s] = *reinterpret_cast<const u32x4 *>(row + d);
         }
+    }
+
+    __device__ __forceinline__ void set_q(const AttnArgs &a)
+    {
         c1 = a.scale_log2;
         c2 = 0.f;
+        acc0 = f32x4{0.f, 0.f, 0.f, 0.f};
         if constexpr (!kRaw) {
+            float amax = 0.f, sum = 0.f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x, y;
+                    unpack16<QT>(q[s][e], x, y);
+                    amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+                    sum += x + y;
+                }
             // q goes to f16 multiplied by the power of two that brings its
             // largest channel to [2^13, 2^14): exact for the channels of a
             // bf16 q down to 2^-26 of it, and off by 2^-33 of it below.
-            amax = head_max(amax);
-            sum = head_sum(sum);
+            amax = column_max(amax);
+            sum = column_sum(sum);
             const int ex = static_cast<int>(__builtin_bit_cast(uint32_t, amax) >> 23) - 127;   // floor(log2 amax)
             const int up = amax > 0.f && ex < 128 ? 13 - ex : 0;
             // 2^up in two factors: up reaches 139
@@ -208,21 +249,25 @@ struct Attn {
             for (int s = 0; s < KS; ++s) {
                 float g8[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g8[e] = f[s][e] * u1 * u2;
-                if constexpr (FMT == PQ_KV_8) {
+                for (int e = 0; e < 4; ++e) unpack16<QT>(q[s][e], g8[2 * e], g8[2 * e + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) q[s][e] = pack16<f16_t>(g8[2 * e], g8[2 * e + 1]);
-                } else {
-                    // the order in which nibbles leave a word (k_operands): 0, 4, then
-                    // 1, 5 sixteen times too large, then 2, 6 and 3, 7 likewise
+                for (int e = 0; e < 8; ++e) g8[e] = g8[e] * u1 * u2;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float f16th = e & 1 ? 0.0625f : 1.f;
-                        q[s][e] = pack16<f16_t>(g8[e] * f16th, g8[e + 4] * f16th);
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (FMT == PQ_KV_8) {
+                        q[s][e] = pack16<f16_t>(g8[2 * e], g8[2 * e + 1]);
+                    } else {
+                        // the order in which nibbles leave a word (scores): 0, 4, then
+                        // 1, 5 sixteen times too large, then 2, 6 and 3, 7 likewise
+                        const float part = e & 1 ? 0.0625f : 1.f;
+                        q[s][e] = pack16<f16_t>(g8[e] * part, g8[e + 4] * part);
                     }
                 }
             }
-            c1 = a.scale_log2 * __builtin_ldexpf(1.f, 24) / u1 / u2;
+            constexpr float mid = FMT == PQ_KV_8 ? 128.f : 8.f;
+            const float start = -mid * 0x1p-24f * (sum * u1 * u2);
+            acc0 = f32x4{start, start, start, start};
+            c1 = a.scale_log2 * 0x1p24f / u1 / u2;
             c2 = a.scale_log2 * sum;
         }
     }
@@ -236,90 +281,75 @@ struct Attn {
         for (int e = 0; e < E; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // What a lane loads of 16 tokens for the first product.
-    static constexpr int KC = kRaw ? KS : KS / 2;
-    struct KTile {
-        u32x4 w[KC];
-        u32x4 par;                  // pairs of tokens 4 kb .. 4 kb + 3
-    };
-    struct VTile {
-        uint32_t w[4][E / (kRaw ? 2 : FMT == PQ_KV_8 ? 4 : 8) ? E / (kRaw ? 2 : FMT == PQ_KV_8 ? 4 : 8) : 1];   // tokens 4 kb + j
-        u32x4 par;
-    };
-    static constexpr int VW = sizeof(VTile::w[0]) / 4;
-
-    // `row`: the page's first row of this head plus t0's offset (wave-uniform)
-    static __device__ __forceinline__ void load_k(const AttnArgs &a, const uint8_t *row, const uint32_t *par, KTile &t)
+    // Rows of the 16 tokens at `row` (wave-uniform).  Channels past dim: any,
+    // q is 0 there.
+    __device__ __forceinline__ void load_k(const AttnArgs &a, int r, int tile, const uint8_t *row)
     {
-        const int lane = threadIdx.x & 63, kb = lane >> 4;
-        const uint8_t *p = row + (lane & 15) * a.token_stride;
+        const uint8_t *p = row + column() * a.token_stride;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            if constexpr (kRaw) {
-                const int d = min(32 * c + 8 * kb, a.dim - 8);          // past dim: any channel, q is 0 there
-                t.w[c] = *reinterpret_cast<const u32x4_a8 *>(p + 2 * d);
+            if constexpr (KW == 2) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p + min(32 * c + 8 * kb(), a.dim / 2 - 8));
+                k[r][tile][c][0] = w[0];
+                k[r][tile][c][1] = w[1];
             } else {
-                const int d = min(64 * c + 16 * kb, a.dim - 16);
-                if constexpr (FMT == PQ_KV_8) {
-                    t.w[c] = *reinterpret_cast<const u32x4_a8 *>(p + d);
-                } else {
-                    const u32x2 w = *reinterpret_cast<const u32x2 *>(p + d / 2);
-                    t.w[c] = u32x4{w[0], w[1], 0, 0};
-                }
+                const int at = kRaw ? 2 * min(32 * c + 8 * kb(), a.dim - 8) : min(64 * c + 16 * kb(), a.dim - 16);
+                const u32x4 w = *reinterpret_cast<const u32x4_a8 *>(p + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) k[r][tile][c][e] = w[e];
             }
         }
-        if constexpr (!kRaw) t.par = *reinterpret_cast<const u32x4 *>(par + 4 * kb);
     }
 
-    static __device__ __forceinline__ void load_v(const AttnArgs &a, const uint8_t *row, const uint32_t *par, VTile &t)
+    __device__ __forceinline__ void load_v(const AttnArgs &a, int r, int tile, const uint8_t *row)
     {
-        const int lane = threadIdx.x & 63, kb = lane >> 4;
-        const int d = min((lane & 15) * E, a.dim - E);
-        const uint8_t *p = row + 4 * kb * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
+        const int d = min(column() * E, a.dim - E);
+        const uint8_t *p = row + 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t *r = p + j * a.token_stride;
+            const uint8_t *t = p + j * a.token_stride;
+            uint32_t(&w)[VW] = v[r][tile][j];
             if constexpr (FMT == PQ_KV_4 && E == 4) {
-                t.w[j][0] = *reinterpret_cast<const uint16_t *>(r);
+                w[0] = *reinterpret_cast<const uint16_t *>(t);
             } else if constexpr (VW == 1) {
-                t.w[j][0] = *reinterpret_cast<const uint32_t *>(r);
+                w[0] = *reinterpret_cast<const uint32_t *>(t);
             } else if constexpr (VW == 2) {
-                const u32x2 w = *reinterpret_cast<const u32x2_a4 *>(r);
-                t.w[j][0] = w[0];
-                t.w[j][1] = w[1];
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(t);
+                w[0] = x[0];
+                w[1] = x[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < VW / 4; ++i) {
-                    const u32x4 w = reinterpret_cast<const u32x4_a8 *>(r)[i];
+                    const u32x4 x = reinterpret_cast<const u32x4_a8 *>(t)[i];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) t.w[j][4 * i + e] = w[e];
+                    for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
                 }
             }
         }
-        if constexpr (!kRaw) t.par = *reinterpret_cast<const u32x4 *>(par + 4 * kb);
     }
 
-    __device__ __forceinline__ f32x4 scores(const KTile &t) const
+    __device__ __forceinline__ f32x4 scores(int r, int tile) const
     {
-        f32x4 c = {0.f, 0.f, 0.f, 0.f};
+        f32x4 c = acc0;
 #pragma unroll
         for (int i = 0; i < KC; ++i) {
+            const uint32_t(&w)[KW] = k[r][tile][i];
             if constexpr (kRaw) {
-                c = mfma16<kF16>(t.w[i], q[i], c);
+                c = mfma16<kF16>(u32x4{w[0], w[1], w[2], w[3]}, q[i], c);
             } else if constexpr (FMT == PQ_KV_8) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     u32x4 f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        f[e] = __builtin_amdgcn_perm(0, t.w[i][2 * s + (e >> 1)], e & 1 ? 0x0c030c02u : 0x0c010c00u);
+                        f[e] = __builtin_amdgcn_perm(0, w[2 * s + (e >> 1)], e & 1 ? 0x0c030c02u : 0x0c010c00u);
                     c = mfma16<kF16>(f, q[2 * i + s], c);
                 }
             } else {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const uint32_t w = t.w[i][s], w8 = w >> 8;
-                    const u32x4 f = {w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
+                    const uint32_t w0 = w[s], w8 = w0 >> 8;
+                    const u32x4 f = {w0 & 0x000F000Fu, w0 & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u};
                     c = mfma16<kF16>(f, q[2 * i + s], c);
                 }
             }
@@ -327,45 +357,59 @@ struct Attn {
         return c;
     }
 
-    // Operand of channel E * (lane % 16) + e: tokens 4 kb + j of tile a, then of b.
-    static __device__ __forceinline__ u32x4 v_operand(const VTile &ta, const VTile &tb, int e)
+    // Operand of channel E * column + e: tokens 4 kb + j of the block's first tile, then of its second.
+    __device__ __forceinline__ u32x4 v_operand(int r, int e) const
     {
         u32x4 f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const VTile &t = i < 2 ? ta : tb;
-            const int j = 2 * (i & 1);
+            const uint32_t *w0 = v[r][i >> 1][2 * (i & 1)], *w1 = v[r][i >> 1][2 * (i & 1) + 1];
             if constexpr (kRaw) {
-                f[i] = __builtin_amdgcn_perm(t.w[j + 1][e >> 1], t.w[j][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+                f[i] = __builtin_amdgcn_perm(w1[e >> 1], w0[e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
             } else if constexpr (FMT == PQ_KV_8) {
                 const uint32_t b = e & 3;
-                f[i] = __builtin_amdgcn_perm(t.w[j + 1][e >> 2], t.w[j][e >> 2], 0x0c000c00u | b | (b + 4) << 16);
+                f[i] = __builtin_amdgcn_perm(w1[e >> 2], w0[e >> 2], 0x0c000c00u | b | (b + 4) << 16);
             } else {
                 const uint32_t b = (e >> 1) & 3, mask = e & 1 ? 0xF0F0F0F0u : 0x0F0F0F0Fu;   // odd channels: 16 n
-                f[i] = __builtin_amdgcn_perm(t.w[j + 1][e >> 3] & mask, t.w[j][e >> 3] & mask, 0x0c000c00u | b | (b + 4) << 16);
+                f[i] = __builtin_amdgcn_perm(w1[e >> 3] & mask, w0[e >> 3] & mask, 0x0c000c00u | b | (b + 4) << 16);
             }
         }
         return f;
     }
 
-    // 32 tokens.  `seen`: bit i for token 4 kb + i of tile a, bit 4 + i of b.
-    __device__ __forceinline__ void step(const KTile &ka, const KTile &kb_, VTile &va, VTile &vb, unsigned seen, bool masked)
+    // First product of all blocks; the lane keeps the scores of its own.
+    __device__ __forceinline__ void first_product(float (&x)[8]) const
     {
-        const f32x4 sa = scores(ka), sb = scores(kb_);
-        float x[8], y[8];           // y = x + log2 s_v: the exponent of the weight of the codes
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const f32x4 sa = scores(r, 0), sb = scores(r, 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float s = i < 4 ? sa[i & 3] : sb[i & 3];
+                x[i] = r == 0 || copy() == r ? s : x[i];
+            }
+        }
+    }
+
+    // Scores to weights, as operands.  `seen`: bit i for token 4 kb + i of the
+    // own block's first tile, bit 4 + i of its second.
+    __device__ __forceinline__ void softmax(float (&x)[8], unsigned seen, bool masked, u32x4 &hi, u32x4 &lo)
+    {
+        float y[8];                 // x + log2 s_v: the exponent of the weight of the codes
         float sv[8], zv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float acc = i < 4 ? sa[i & 3] : sb[i & 3];
             if constexpr (kRaw) {
-                x[i] = y[i] = acc * c1;
+                y[i] = x[i] = x[i] * c1;
             } else {
-                const uint32_t kp = i < 4 ? ka.par[i & 3] : kb_.par[i & 3], vp = i < 4 ? va.par[i & 3] : vb.par[i & 3];
-                sv[i] = __builtin_bit_cast(float, vp << 16);
-                zv[i] = __builtin_bit_cast(float, vp & 0xFFFF0000u);
-                x[i] = __builtin_fmaf(__builtin_bit_cast(float, kp << 16), acc * c1,
-                                      __builtin_bit_cast(float, kp & 0xFFFF0000u) * c2);
-                y[i] = x[i] + __builtin_amdgcn_logf(sv[i]);
+                constexpr float mid = FMT == PQ_KV_8 ? 128.f : 8.f;
+                const uint32_t kw = kpar[i >> 2][i & 3], vw = vpar[i >> 2][i & 3];
+                const float sk = __builtin_bit_cast(float, kw << 16), zk = __builtin_bit_cast(float, kw & 0xFFFF0000u);
+                sv[i] = __builtin_bit_cast(float, vw << 16);
+                zv[i] = __builtin_bit_cast(float, vw & 0xFFFF0000u);
+                x[i] = __builtin_fmaf(sk, x[i] * c1, __builtin_fmaf(sk, mid, zk) * c2);
+                // the bits of a positive float are 2^23 (127 + log2) to within 0.09 octaves
+                y[i] = __builtin_fmaf(static_cast<float>(vw << 16), 0x1p-23f, x[i]) - 127.f;
             }
         }
         if (masked) {
@@ -380,16 +424,13 @@ struct Attn {
                 } else {
                     // 0 times what lies there must be 0
 #pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        uint32_t &r = i < 4 ? va.w[i & 3][w] : vb.w[i & 3][w];
-                        r = on ? r : 0u;
-                    }
+                    for (int w = 0; w < VW; ++w) v[0][i >> 2][i & 3][w] = on ? v[0][i >> 2][i & 3][w] : 0u;
                 }
             }
         }
-        float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-        if (__ballot(top > m + kSlack)) {           // also the first tile: m is -inf
-            const float mn = fmaxf(m, head_max(top));
+        const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+        if (__ballot(top > m + kSlack)) {           // also the first step: m is -inf
+            const float mn = fmaxf(m, column_max(top));
             const float f = m == mn ? 1.f : exp2_fast(m - mn);
             m = mn;
             l *= f;
@@ -410,10 +451,6 @@ struct Attn {
                 zsum = __builtin_fmaf(p, zv[i], zsum);
             }
         }
-        // The weights as the sum of two 16-bit values: rounded to one, each
-        // token's share would be off by 2^-9 (bf16) and the output by as much
-        // as its own rounding again.
-        u32x4 hi, lo;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             hi[i] = pack16<OT>(w[2 * i], w[2 * i + 1]);
@@ -421,11 +458,27 @@ struct Attn {
             unpack16<OT>(hi[i], h0, h1);
             lo[i] = pack16<OT>(w[2 * i] - h0, w[2 * i + 1] - h1);
         }
+    }
+
+    __device__ __forceinline__ void second_product(const u32x4 &hi, const u32x4 &lo)
+    {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const u32x4 f = v_operand(va, vb, e);
-            o[e] = mfma16<kF16>(f, hi, o[e]);
-            o[e] = mfma16<kF16>(f, lo, o[e]);
+        for (int r = 0; r < R; ++r) {
+            u32x4 h = hi, w = lo;
+            if constexpr (R > 1) {
+                const bool own = copy() == r;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = own ? hi[i] : 0u;
+                    w[i] = own ? lo[i] : 0u;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const u32x4 f = v_operand(r, e);
+                o[e] = mfma16<kF16>(f, h, o[e]);
+                o[e] = mfma16<kF16>(f, w, o[e]);
+            }
         }
     }
 
@@ -437,97 +490,198 @@ struct Attn {
     }
 };
 
-template <typename QT, int FMT, int DP>
+// out and lse of 4 channels of a row from its sums.
+template <typename QT>
+__device__ __forceinline__ void write_out(const AttnArgs &a, int b, int hq, int d, float M, float L, f32x4 v)
+{
+    // L is 0 only where every token lies in a hidden page
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    *reinterpret_cast<u32x2 *>(a.out + b * a.out_bs + hq * a.out_hs + d) =
+        u32x2{pack16<QT>(v[0] * inv, v[1] * inv), pack16<QT>(v[2] * inv, v[3] * inv)};
+    if (d == 0 && a.lse)
+        a.lse[static_cast<int64_t>(b) * a.q_heads + hq] =
+            L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+}
+
+// A row (sequence, cache head, head tile) of a share, as its waves see it.
+struct Row {
+    int b, kvh, gt;
+    int row0, n, stop;              // its first step, its steps; where the share's part of it ends
+    Range r;
+    int t0, count;                  // the wave's first token; its steps (every kWaves-th)
+};
+
+template <typename QT, int FMT, int DP, int R>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs a)
 {
-    using A = Attn<QT, FMT, DP>;
-    constexpr int E = A::E;
+    using A = Attn<QT, FMT, DP, R>;
+    constexpr int E = A::E, kUnit = A::kUnit, kCols = A::kCols;
     constexpr int kPad = DP + 4;
-    __shared__ int64_t s_pre[kMaxBatch + 1];
-    __shared__ int64_t s_wsum[4];
-    __shared__ float s_m[4][16], s_l[4][16], s_z[4][16];
-    __shared__ __align__(16) float s_o[4 * 16 * kPad];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kb = lane >> 4, head = lane & 15;
-    tile_prefix(a, s_pre, s_wsum);
+    constexpr int kIds = 2 * R, kBatch = 64 / kIds;         // page ids of a step; steps whose ids a wave holds
+    __shared__ int s_pre[kMaxBatch + 1], s_len[kMaxBatch];
+    __shared__ int s_wsum[kWaves];
+    __shared__ float s_m[kWaves][16], s_l[kWaves][16], s_z[kWaves][16];
+    __shared__ __align__(16) float s_o[kWaves * 16 * kPad];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kb = A::kb(), column = A::column();
     const int vheads = a.heads * a.gtiles;
-    const int64_t total = s_pre[a.batch] * vheads;
-    const int64_t per = (total + a.shares - 1) / a.shares;
-    const int64_t begin = blockIdx.x * per, end = begin + per < total ? begin + per : total;
-    if (begin >= end) return;
-    int b = 0;
-    {
-        int hi = a.batch - 1;                       // last b whose rows start at or before `begin`
-        while (b < hi) {
-            const int mid = (b + hi + 1) >> 1;
-            if (s_pre[mid] * vheads <= begin) b = mid;
+    Cut cut = {};
+    int begin = 0, end = 0;
+    if (a.shares) {
+        step_prefix(a, kUnit, s_len, s_pre, s_wsum);
+        const int total = s_pre[a.batch] * vheads;
+        cut = Cut{total / a.shares, total % a.shares};
+        begin = cut.begin(blockIdx.x);
+        end = cut.begin(blockIdx.x + 1);
+        if (begin >= end) return;
+    }
+    const int in_page = (1 << a.page_log2) - 1;
+
+    auto row_of = [&](int at, int b) {              // the row of step `at`, in sequence b or later
+        Row w;
+        while (s_pre[b + 1] * vheads <= at) ++b;    // also past sequences without steps
+        w.b = __builtin_amdgcn_readfirstlane(b);
+        const int p0 = __builtin_amdgcn_readfirstlane(s_pre[w.b]);
+        w.n = __builtin_amdgcn_readfirstlane(s_pre[w.b + 1]) - p0;
+        const int vh = (at - p0 * vheads) / w.n;
+        w.row0 = p0 * vheads + vh * w.n;
+        w.kvh = vh / a.gtiles;
+        w.gt = vh - w.kvh * a.gtiles;
+        w.stop = min(w.row0 + w.n, end);
+        w.r = range_of(a, __builtin_amdgcn_readfirstlane(s_len[w.b]));
+        w.t0 = w.r.base + (at - w.row0 + wave) * kUnit;
+        w.count = (w.stop - at - wave + kWaves - 1) / kWaves;
+        return w;
+    };
+    auto load_ids = [&](const Row &w, int i0) {     // page ids of steps i0 .. i0 + kBatch - 1, one a lane
+        const int i = i0 + lane / kIds;
+        const int t = w.t0 + i * (kWaves * kUnit) + lane % kIds * 16;
+        int id = -1;
+        if (i < w.count && t < w.r.len) {
+            id = a.table[w.b * a.table_stride + (t >> a.page_log2)];
+            if (id < 0 || id >= a.num_pages) id = -1;
+        }
+        return id;
+    };
+    A st;
+    // hidden tiles are read from page 0 and masked
+    auto row_at = [&](const Row &w, int held, int i, int tile) {
+        const int id = max(__builtin_amdgcn_readlane(held, (i % kBatch) * kIds + tile), 0);
+        const int off = (w.t0 + i * (kWaves * kUnit) + tile * 16) & in_page;
+        return id * a.page_stride + w.kvh * a.head_stride + static_cast<int64_t>(off) * a.token_stride;
+    };
+    auto load_keys = [&](const Row &w, int held, int i) {
+#pragma unroll
+        for (int t = 0; t < kIds; ++t) st.load_k(a, t >> 1, t & 1, a.k + row_at(w, held, i, t));
+    };
+    auto load_values = [&](const Row &w, int held, int i) {
+#pragma unroll
+        for (int t = 0; t < kIds; ++t) st.load_v(a, t >> 1, t & 1, a.v + row_at(w, held, i, t));
+    };
+    auto load_pairs = [&](const Row &w, int held, int i) {
+        if constexpr (!A::kRaw) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tile = 2 * A::copy() + t;
+                const int id = max(__shfl(held, (i % kBatch) * kIds + tile), 0);
+                const int off = (w.t0 + i * (kWaves * kUnit) + tile * 16) & in_page;
+                const int64_t p = ((static_cast<int64_t>(id) * a.heads + w.kvh) << a.page_log2) + off + 4 * kb;
+                st.kpar[t] = *reinterpret_cast<const u32x4 *>(a.kp + p);
+                st.vpar[t] = *reinterpret_cast<const u32x4 *>(a.vp + p);
+            }
+        }
+    };
+    auto start = [&](const Row &w, int held) {      // first loads of a row
+        if (w.count > 0) {
+            load_keys(w, held, 0);
+            load_pairs(w, held, 0);
+            load_values(w, held, 0);
+        }
+        st.load_q(a, w.b, w.kvh, w.gt);
+    };
+
+    Row w;
+    if (a.shares) {
+        int b0 = 0, hi = a.batch - 1;               // last sequence whose rows start at or before `begin`
+        while (b0 < hi) {
+            const int mid = (b0 + hi + 1) >> 1;
+            if (s_pre[mid] * vheads <= begin) b0 = mid;
             else hi = mid - 1;
         }
+        w = row_of(begin, b0);
+    } else {                                        // the block's own row
+        w.b = blockIdx.x / vheads;
+        const int vh = blockIdx.x - w.b * vheads;
+        w.kvh = vh / a.gtiles;
+        w.gt = vh - w.kvh * a.gtiles;
+        w.r = range_of(a, a.lens[w.b]);
+        w.row0 = 0;
+        w.n = w.stop = end = w.r.steps(kUnit);
+        w.t0 = w.r.base + wave * kUnit;
+        w.count = (w.n - wave + kWaves - 1) / kWaves;
     }
-    A st;
-    for (int64_t at = begin; at < end;) {
-        while (s_pre[b + 1] * vheads <= at) ++b;    // also past sequences without tiles
-        const int64_t n = s_pre[b + 1] - s_pre[b];
-        const int vh = static_cast<int>((at - s_pre[b] * vheads) / n);
-        const int64_t row0 = s_pre[b] * vheads + vh * n;
-        const int kvh = vh / a.gtiles, gt = vh - kvh * a.gtiles;
-        const int64_t stop = row0 + n < end ? row0 + n : end;
-        const Range r = range_of(a, b);
-        const int32_t *pages = a.table + b * a.table_stride;
-        st.load_q(a, b, kvh, gt);
+    int ids = load_ids(w, 0);
+    start(w, ids);
+    for (;;) {
+        st.set_q(a);
         st.clear();
-        // 64 pages' ids at a time, one a lane: 32 tiles of two 16-token halves
-        for (int64_t j0 = at - row0; j0 < stop - row0; j0 += 32) {
-            const int count = static_cast<int>(stop - row0 - j0 < 32 ? stop - row0 - j0 : 32);
-            const int64_t t_lane = r.base + (j0 + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16;
-            int id = -1;
-            if ((lane >> 1) < count && t_lane < r.len) {
-                id = pages[t_lane >> a.page_log2];
-                if (id < 0 || id >= a.num_pages) id = -1;
-            }
-            for (int j = 0; j < count; ++j) {
-                const int64_t t = r.base + (j0 + j) * kTile + wave * 32;
-                if (t >= r.len) break;
-                typename A::KTile ka, kc;
-                typename A::VTile va, vc;
-                const int pa = __builtin_amdgcn_readlane(id, 2 * j), pb = __builtin_amdgcn_readlane(id, 2 * j + 1);
-                const bool masked = pa < 0 || pb < 0 || t < r.first || t + 32 > r.len;
-                const int in_page = (1 << a.page_log2) - 1;
-                const int oa = static_cast<int>(t) & in_page, ob = static_cast<int>(t + 16) & in_page;
-                const int64_t page_a = pa < 0 ? 0 : pa, page_b = pb < 0 ? 0 : pb;
-                const int64_t ra = page_a * a.page_stride + kvh * a.head_stride + static_cast<int64_t>(oa) * a.token_stride;
-                const int64_t rb = page_b * a.page_stride + kvh * a.head_stride + static_cast<int64_t>(ob) * a.token_stride;
-                const int64_t qa = ((page_a * a.heads + kvh) << a.page_log2) + oa;
-                const int64_t qb = ((page_b * a.heads + kvh) << a.page_log2) + ob;
-                A::load_k(a, a.k + ra, a.kp + qa, ka);
-                A::load_k(a, a.k + rb, a.kp + qb, kc);
-                A::load_v(a, a.v + ra, a.vp + qa, va);
-                A::load_v(a, a.v + rb, a.vp + qb, vc);
-                unsigned seen = 0xFF;
-                if (masked) {
-                    seen = 0;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t u = t + (i >> 2) * 16 + 4 * kb + (i & 3);
-                        if ((i < 4 ? pa : pb) >= 0 && u >= r.first && u < r.len) seen |= 1u << i;
-                    }
-                }
-                st.step(ka, kc, va, vc, seen, masked);
-            }
+        // the next row's page ids come along with this row
+        const bool follows = w.stop < end;
+        Row next = w;
+        int next_ids = -1;
+        if (follows) {
+            next = row_of(w.stop, w.b);
+            next_ids = load_ids(next, 0);
         }
-        // join the four waves
-        __syncthreads();                            // the last row's s_o has been read
-        const float l_all = head_sum(st.l), z_all = head_sum(st.zsum);
+        int ids_after = ids;
+        for (int i = 0; i < w.count; ++i) {
+            if (i % kBatch == 0 && i + kBatch < w.count) ids_after = load_ids(w, i + kBatch);
+            float x[8];
+            st.first_product(x);
+            const int here = ids;
+            if ((i + 1) % kBatch == 0) ids = ids_after;
+            const bool more = i + 1 < w.count;
+            if (more) load_keys(w, ids, i + 1);
+            const int own = 2 * A::copy(), t = w.t0 + i * (kWaves * kUnit);
+            const int id_a = __shfl(here, (i % kBatch) * kIds + own), id_b = __shfl(here, (i % kBatch) * kIds + own + 1);
+            const bool masked = __ballot(id_a < 0 || id_b < 0) != 0 || t < w.r.first || t + kUnit > w.r.len;
+            unsigned seen = 0xFF;
+            if (masked) {
+                seen = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int u = t + own * 16 + 4 * kb + (e >> 2) * 16 + (e & 3);
+                    if ((e < 4 ? id_a : id_b) >= 0 && u >= w.r.first && u < w.r.len) seen |= 1u << e;
+                }
+            }
+            u32x4 hi, lo;
+            st.softmax(x, seen, masked, hi, lo);
+            if (more) load_pairs(w, ids, i + 1);
+            st.second_product(hi, lo);
+            if (more) load_values(w, ids, i + 1);
+        }
+        if (follows) start(next, next_ids);         // its loads pass while this row is joined
+        // join the waves and the copies of the columns
+        const float l_all = column_sum(st.l), z_all = column_sum(st.zsum);
+        __syncthreads();                            // the last row's s_m and s_o have been read
         if (kb == 0) {
-            s_m[wave][head] = st.m;
-            s_l[wave][head] = l_all;
-            s_z[wave][head] = z_all;
+            s_m[wave][column] = st.m;
+            s_l[wave][column] = l_all;
+            s_z[wave][column] = z_all;
         }
         __syncthreads();
-        const float mx = fmaxf(fmaxf(s_m[0][head], s_m[1][head]), fmaxf(s_m[2][head], s_m[3][head]));
-        const float f = st.m == mx ? 1.f : exp2_fast(st.m - mx);
-        const int rows = min(16, a.group - gt * 16);
-        if (head < rows) {
-            float *so = s_o + (wave * 16 + head) * kPad;
+        const int rows = min(kCols, a.group - w.gt * 16);
+        const int g_own = column % kCols;
+        auto top_of = [&](int g) {
+            float M = -__builtin_inff();
+            for (int v = 0; v < kWaves; ++v)
+#pragma unroll
+                for (int c = 0; c < R; ++c) M = fmaxf(M, s_m[v][c * kCols + g]);
+            return M;
+        };
+        if (g_own < rows) {
+            const float M = top_of(g_own), f = st.m == M ? 1.f : exp2_fast(st.m - M);
+            float *so = s_o + (wave * 16 + column) * kPad;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -537,109 +691,165 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
                               st.o[e + 2][i] * (f * A::o_unit(0)), st.o[e + 3][i] * (f * A::o_unit(1))};
         }
         __syncthreads();
-        const bool whole = row0 >= begin && row0 + n <= end;
-        const int64_t slot = part_slot(blockIdx.x, row0, per);
+        const bool whole = w.row0 >= begin && w.row0 + w.n <= end;
+        const int slot = cut.slot(blockIdx.x, w.row0), hq0 = w.kvh * a.group + w.gt * 16;
         for (int i = tid * 4; i < rows * DP; i += 1024) {
             const int g = i / DP, d = i - g * DP;
             if (d >= a.dim) continue;
-            const float M = fmaxf(fmaxf(s_m[0][g], s_m[1][g]), fmaxf(s_m[2][g], s_m[3][g]));
+            const float M = top_of(g);
             float L = 0.f, Z = 0.f;
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            for (int w = 0; w < 4; ++w) {
-                const float fw = s_m[w][g] == M ? 1.f : exp2_fast(s_m[w][g] - M);
-                L += s_l[w][g] * fw;
-                Z += s_z[w][g] * fw;
-                v += *reinterpret_cast<const f32x4 *>(s_o + (w * 16 + g) * kPad + d);
-            }
+            for (int u = 0; u < kWaves; ++u)
+#pragma unroll
+                for (int c = 0; c < R; ++c) {
+                    const int col = c * kCols + g;
+                    const float fw = s_m[u][col] == M ? 1.f : exp2_fast(s_m[u][col] - M);
+                    L += s_l[u][col] * fw;
+                    Z += s_z[u][col] * fw;
+                    v += *reinterpret_cast<const f32x4 *>(s_o + (u * 16 + col) * kPad + d);
+                }
             v += Z;
             if (whole) {
-                // L is 0 only if every token lies in a hidden page
-                const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-                const int64_t hq = static_cast<int64_t>(kvh) * a.group + gt * 16 + g;
-                u32x2 w2 = {pack16<QT>(v[0] * inv, v[1] * inv), pack16<QT>(v[2] * inv, v[3] * inv)};
-                *reinterpret_cast<u32x2 *>(a.out + b * a.out_bs + hq * a.out_hs + d) = w2;
-                if (d == 0 && a.lse)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + hq] =
-                        L == 0.f ? -__builtin_inff() : (M - A::kShift + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+                write_out<QT>(a, w.b, hq0 + g, d, M - A::kShift, L, v);
             } else {
-                *reinterpret_cast<f32x4 *>(a.part_o + (slot * a.group_rows + g) * a.dim + d) = v;
-                if (d == 0) {
-                    a.part_ml[(slot * a.group_rows + g) * 2] = M - A::kShift;
-                    a.part_ml[(slot * a.group_rows + g) * 2 + 1] = L;
-                }
+                const int64_t at = static_cast<int64_t>(slot) * a.group_rows + g;
+                *reinterpret_cast<f32x4 *>(a.part_o + at * a.dim + d) = v;
+                if (d == 0) a.part_ml[at] = f32x2{M - A::kShift, L};
             }
         }
-        at = stop;
+        if (a.shares && w.row0 >= begin && tid == 0)        // for the join: whose partials make up the row
+            a.spans[(w.b * a.heads + w.kvh) * a.gtiles + w.gt] =
+                make_int2(slot, cut.share_of(w.row0 + w.n - 1));
+        if (!follows) break;
+        w = next;
+        ids = next_ids;
     }
 }
 
 // Joins the shares of the rows that span several, in order, and writes the
-// rows without a token.  One block per (sequence, cache head, head tile).
+// rows without a token.  One block per query head: its thread groups take
+// every so many shares each, and their sums meet in LDS.
 template <typename QT>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
 {
-    __shared__ int64_t s_pre[kMaxBatch + 1];
-    __shared__ int64_t s_wsum[4];
-    tile_prefix(a, s_pre, s_wsum);
-    const int vheads = a.heads * a.gtiles;
-    const int64_t total = s_pre[a.batch] * vheads;
-    const int64_t per = (total + a.shares - 1) / a.shares;
-    const int b = blockIdx.x / vheads, vh = blockIdx.x - b * vheads;
-    const int kvh = vh / a.gtiles, gt = vh - kvh * a.gtiles;
-    const int rows = min(16, a.group - gt * 16);
-    const int64_t n = s_pre[b + 1] - s_pre[b];
-    const int64_t row0 = s_pre[b] * vheads + vh * n;
-    const int64_t first = n ? row0 / per : 0, last = n ? (row0 + n - 1) / per : -1;
-    if (first == last) return;
-    for (int i = threadIdx.x * 4; i < rows * a.dim; i += 1024) {
-        const int g = i / a.dim, d = i - g * a.dim;
-        float M = -__builtin_inff(), L = 0.f;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t s = first; s <= last; ++s)
-            M = fmaxf(M, a.part_ml[(part_slot(s, row0, per) * a.group_rows + g) * 2]);
-        for (int64_t s = first; s <= last; ++s) {
-            const int64_t at = part_slot(s, row0, per) * a.group_rows + g;
-            const float ms = a.part_ml[at * 2];
-            const float f = ms == M ? 1.f : exp2_fast(ms - M);
-            L = __builtin_fmaf(a.part_ml[at * 2 + 1], f, L);
-            const f32x4 p = *reinterpret_cast<const f32x4 *>(a.part_o + at * a.dim + d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(p[e], f, v[e]);
-        }
-        const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-        const int64_t hq = static_cast<int64_t>(kvh) * a.group + gt * 16 + g;
-        u32x2 w2 = {pack16<QT>(v[0] * inv, v[1] * inv), pack16<QT>(v[2] * inv, v[3] * inv)};
-        *reinterpret_cast<u32x2 *>(a.out + b * a.out_bs + hq * a.out_hs + d) = w2;
-        if (d == 0 && a.lse)
-            a.lse[static_cast<int64_t>(b) * a.q_heads + hq] =
-                L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+    __shared__ float s_w[kMaxShares], s_red[2 * kWaves];
+    __shared__ __align__(16) float s_v[1024];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int b = blockIdx.x / a.q_heads, hq = blockIdx.x - b * a.q_heads;
+    const int kvh = hq / a.group, gi = hq - kvh * a.group, gt = gi / 16, g = gi - gt * 16;
+    const int row = (b * a.heads + kvh) * a.gtiles + gt;
+    const Range r = range_of(a, a.lens[b]);
+    const int2 span = a.spans[row];                 // unset for a row without steps
+    const int quads = a.dim / 4, groups = 256 / quads, q = tid % quads, part = tid / quads;
+    if (r.len <= r.first) {
+        if (part == 0) write_out<QT>(a, b, hq, 4 * q, 0.f, 0.f, f32x4{0.f, 0.f, 0.f, 0.f});
+        return;
     }
+    const int first = span.x >> 1, n = span.y - first + 1;
+    if (n == 1) return;                             // written by its share
+    auto slot_of = [&](int s) { return static_cast<int64_t>(s == 0 ? span.x : 2 * (first + s)) * a.group_rows + g; };
+    const bool on = part < groups;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < n; s0 += 8 * groups) {
+        f32x4 p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = s0 + part + k * groups;
+            p[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (on && s < n) p[k] = *reinterpret_cast<const f32x4 *>(a.part_o + slot_of(s) * a.dim + 4 * q);
+        }
+        if (s0 == 0) {                              // meanwhile the weights: (m, l) of up to two shares a thread
+            f32x2 ml[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ml[k] = tid + 256 * k < n ? a.part_ml[slot_of(tid + 256 * k)] : f32x2{-__builtin_inff(), 0.f};
+            float M = fmaxf(ml[0][0], ml[1][0]);
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+            if (lane == 0) s_red[wave] = M;
+            __syncthreads();
+            M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+            float L = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float f = ml[k][0] == M ? 1.f : exp2_fast(ml[k][0] - M);
+                if (tid + 256 * k < n) s_w[tid + 256 * k] = f;
+                L = __builtin_fmaf(ml[k][1], f, L);
+            }
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) L += __shfl_xor(L, o);
+            if (lane == 0) s_red[kWaves + wave] = L;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int s = s0 + part + k * groups;
+            const float f = on && s < n ? s_w[s] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(p[k][e], f, v[e]);
+        }
+    }
+    *reinterpret_cast<f32x4 *>(s_v + 4 * tid) = v;
+    __syncthreads();
+    if (part > 0) return;
+    for (int k = 1; k < groups; ++k) v += *reinterpret_cast<const f32x4 *>(s_v + 4 * (k * quads + q));
+    write_out<QT>(a, b, hq, 4 * q, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])),
+                  s_red[kWaves] + s_red[kWaves + 1] + s_red[kWaves + 2] + s_red[kWaves + 3], v);
+}
+
+// Rows of at most this many tokens are not split: one block takes such a row
+// in kWholeRow / 128 rounds, and a second launch would cost more.
+constexpr int kWholeRow = 512;
+
+template <typename QT, int FMT, int DP, int R>
+void launch_one(AttnArgs a, int64_t longest, hipStream_t s)
+{
+    const int unit = 32 * R;
+    const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * a.gtiles;
+    if (longest <= kWholeRow) {
+        a.shares = 0;
+        hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
+        return;
+    }
+    const int64_t want = (rows * ((longest + unit - 1) / unit) + kWaves - 1) / kWaves;    // a step per wave at least
+    a.shares = static_cast<int>(want > kMaxShares ? kMaxShares : want);
+    hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R>), dim3(static_cast<unsigned>(a.shares)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_attn_join<QT>, dim3(static_cast<unsigned>(a.batch * a.q_heads)), dim3(256), 0, s, a);
+}
+
+template <typename QT, int FMT, int DP>
+void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
+{
+    // Two copies of the heads in the columns where the group leaves room.
+    // 16-bit rows take none: their bytes outlast the softmax.
+    if constexpr (FMT != PQ_KV_16) {
+        if (a.group <= 8) return launch_one<QT, FMT, DP, 2>(a, longest, s);
+    }
+    launch_one<QT, FMT, DP, 1>(a, longest, s);
 }
 
 template <typename QT, int FMT>
-void launch_dim(const AttnArgs &a, hipStream_t s)
+void launch_dim(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
-    const dim3 g(static_cast<unsigned>(a.shares)), t(256);
-    if (a.dim <= 64) hipLaunchKernelGGL((k_attn_decode<QT, FMT, 64>), g, t, 0, s, a);
-    else if (a.dim <= 128) hipLaunchKernelGGL((k_attn_decode<QT, FMT, 128>), g, t, 0, s, a);
-    else hipLaunchKernelGGL((k_attn_decode<QT, FMT, 256>), g, t, 0, s, a);
+    if (a.dim <= 64) launch_copies<QT, FMT, 64>(a, longest, s);
+    else if (a.dim <= 128) launch_copies<QT, FMT, 128>(a, longest, s);
+    else launch_copies<QT, FMT, 256>(a, longest, s);
 }
 
 template <typename QT>
-pq_status launch_attn(int format, const AttnArgs &a, hipStream_t s)
+pq_status launch_attn(int format, const AttnArgs &a, int64_t longest, hipStream_t s)
 {
-    if (format == PQ_KV_16) launch_dim<QT, PQ_KV_16>(a, s);
-    else if (format == PQ_KV_8) launch_dim<QT, PQ_KV_8>(a, s);
-    else launch_dim<QT, PQ_KV_4>(a, s);
-    if (hipGetLastError() != hipSuccess) return PQ_ERR_HIP;
-    hipLaunchKernelGGL(k_attn_join<QT>, dim3(static_cast<unsigned>(a.batch * a.heads * a.gtiles)), dim3(256), 0, s, a);
+    if (format == PQ_KV_16) launch_dim<QT, PQ_KV_16>(a, longest, s);
+    else if (format == PQ_KV_8) launch_dim<QT, PQ_KV_8>(a, longest, s);
+    else launch_dim<QT, PQ_KV_4>(a, longest, s);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
-int64_t attn_workspace(int dim, int group)
+// Workspace: o, then (m, l), then the spans.
+int64_t part_rows(int group) { return static_cast<int64_t>(2) * kMaxShares * (group < 16 ? group : 16); }
+int64_t attn_workspace(const pq_kv_cache &c, int64_t batch, int group)
 {
-    const int64_t rows = group < 16 ? group : 16;
-    return 2 * kMaxShares * rows * (dim + 4) * 4;   // o, then m and l (padded to 16 bytes)
+    const int64_t n = batch < kMaxBatch ? batch : kMaxBatch;
+    return part_rows(group) * (c.dim + 2) * 4 + n * c.heads * ((group + 15) / 16) * 8;
 }
 
 }  // namespace
@@ -652,7 +862,7 @@ int64_t pq_attn_decode_workspace_bytes(const pq_kv_cache *cache, int64_t batch, 
     using namespace pq;
     if (kv_cache_status(cache) != PQ_OK || batch < 0 || q_heads < 1 || q_heads % cache->heads) return -1;
     if (batch == 0) return 0;
-    return attn_workspace(cache->dim, static_cast<int>(q_heads / cache->heads));
+    return (attn_workspace(*cache, batch, static_cast<int>(q_heads / cache->heads)) + 15) / 16 * 16;
 }
 
 pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, int64_t q_heads, const void *q,
@@ -668,7 +878,7 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     if (q_dtype != PQ_BF16 && q_dtype != PQ_F16) return PQ_ERR_MODE;
     if (c.format == PQ_KV_16 && c.dtype != q_dtype) return PQ_ERR_MODE;
     if (batch < 0 || batch > INT32_MAX || q_heads < 1 || q_heads > 65535 || q_heads % c.heads) return PQ_ERR_SHAPE;
-    if (max_pages < 0 || max_pages > (int64_t(1) << 31) / c.page_size || table_stride < 0) return PQ_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (int64_t(1) << 30) / c.page_size || table_stride < 0) return PQ_ERR_SHAPE;
     if (((q_batch_stride | q_head_stride | out_batch_stride | out_head_stride) & 7) != 0) return PQ_ERR_SHAPE;
     if (!std::isfinite(scale) || window < 0 || max_len < 0) return PQ_ERR_ARG;
     if (batch == 0) return PQ_OK;
@@ -677,7 +887,7 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(lse)) % 4)
         return PQ_ERR_ALIGN;
     const int group = static_cast<int>(q_heads / c.heads);
-    if (workspace_bytes < attn_workspace(c.dim, group)) return PQ_ERR_ARG;
+    if (workspace_bytes < attn_workspace(c, batch, group)) return PQ_ERR_ARG;
     AttnArgs a = {};
     a.k = static_cast<const uint8_t *>(c.k);
     a.v = static_cast<const uint8_t *>(c.v);
@@ -695,12 +905,12 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     a.q_hs = q_head_stride;
     a.table = block_table;
     a.table_stride = table_stride;
-    a.max_tokens = max_pages * c.page_size;
+    a.max_tokens = static_cast<int>(max_pages * c.page_size);
     a.lens = lens;
     a.group = group;
     a.gtiles = (group + 15) / 16;
     a.group_rows = group < 16 ? group : 16;
-    a.window = window;
+    a.window = window < INT32_MAX ? static_cast<int>(window) : 0;   // longer than any sequence: everything
     a.scale_log2 = static_cast<float>(scale * 1.4426950408889634074);
     a.out = static_cast<uint16_t *>(out);
     a.out_bs = out_batch_stride;
@@ -708,22 +918,28 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     a.lse = lse;
     a.q_heads = static_cast<int>(q_heads);
     a.part_o = static_cast<float *>(workspace);
-    a.part_ml = a.part_o + static_cast<int64_t>(2) * kMaxShares * a.group_rows * c.dim;
-    int64_t longest = max_len > 0 && max_len < a.max_tokens ? max_len : a.max_tokens;
+    a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + part_rows(group) * c.dim);
+    a.spans = reinterpret_cast<int2 *>(a.part_ml + part_rows(group));
+    // lens past max_len count as max_len: rows are then known to be short
+    if (max_len > 0 && max_len < a.max_tokens) a.max_tokens = static_cast<int>(max_len);
+    int64_t longest = a.max_tokens;
     if (window > 0 && longest > window + 15) longest = window + 15;   // its first tile may start 15 tokens early
-    const int64_t tiles = (longest + kTile - 1) / kTile;
+    // the kernel counts steps of at least 32 tokens in 32 bits
+    const int64_t row_steps = (static_cast<int64_t>(a.max_tokens) + 31) / 32 + 1;
+    int64_t most = INT32_MAX / (row_steps * c.heads * a.gtiles);
+    if (most < 1) return PQ_ERR_SHAPE;
+    if (most > kMaxBatch) most = kMaxBatch;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    for (int64_t b0 = 0; b0 < batch; b0 += kMaxBatch) {
+    for (int64_t b0 = 0; b0 < batch; b0 += most) {
         AttnArgs x = a;
-        x.batch = static_cast<int>(batch - b0 < kMaxBatch ? batch - b0 : kMaxBatch);
+        x.batch = static_cast<int>(batch - b0 < most ? batch - b0 : most);
         x.q += b0 * q_batch_stride;
         x.out += b0 * out_batch_stride;
         if (x.lse) x.lse += b0 * q_heads;
         if (x.table) x.table += b0 * table_stride;
         x.lens += b0;
-        int64_t shares = static_cast<int64_t>(x.batch) * c.heads * a.gtiles * tiles;
-        x.shares = static_cast<int>(shares < 1 ? 1 : shares > kMaxShares ? kMaxShares : shares);
-        const pq_status r = q_dtype == PQ_BF16 ? launch_attn<bf16_t>(c.format, x, s) : launch_attn<f16_t>(c.format, x, s);
+        const pq_status r = q_dtype == PQ_BF16 ? launch_attn<bf16_t>(c.format, x, longest, s)
+                                               : launch_attn<f16_t>(c.format, x, longest, s);
         if (r != PQ_OK) return r;
     }
     return PQ_OK;

@@ -543,7 +543,7 @@ def pq_attn_decode_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> 
 
 
 def attn_workspace(cache: KVCache, batch: int, q_heads: int, device="cuda") -> torch.Tensor:
-    """A workspace for pq_attn_decode calls of this size, for the caller to keep."""
+    """A workspace for pq_attn_decode calls of up to this size, for the caller to keep."""
     n = pq_attn_decode_workspace_bytes(cache, batch, q_heads)
     if n < 0:
         raise PQError(2, "pq_attn_decode_workspace_bytes")

@@ -687,16 +687,18 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
  *                Only the entries of attended tokens are used; a page id
  *                outside the cache hides its tokens
  *   lens         in [batch] int32: tokens in the cache, the new one among
- *                them, clamped to [0, max_pages * page_size].  Nothing to
+ *                them, clamped to [0, max_pages * page_size] (at most 2^30).  Nothing to
  *                attend to gives out = 0 and lse = -inf; what lies in the
  *                cache past len or before the window is never used, NaN and
  *                infinities included
  *   window       attended tokens, 0 for all of them
- *   max_len      an upper bound of lens that sizes the launch (0: max_pages *
- *                page_size); the result for longer sequences is still right
+ *   max_len      an upper bound of lens that sizes the launch; longer ones
+ *                count as max_len (0: max_pages * page_size)
  *   lse          out [batch, q_heads] fp32, or NULL
  *   workspace    device memory of pq_attn_decode_workspace_bytes(cache,
- *                batch, q_heads) bytes, 16-byte aligned
+ *                batch, q_heads) bytes, 16-byte aligned; its contents on
+ *                entry do not matter.  Calls that overlap, on different
+ *                streams, need different workspaces
  * For fixed arguments the result is the same in every run (max_len and the
  * other sequences of a batch decide where a sequence is split, and with it
  * the order of its sums).

@@ -129,8 +129,13 @@ def test_split_rows(pq, fmt, lens):
     c.check(out, lse)
     again = c.run(pq)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])         # the same in every run
-    for hint in (1, 130, 1 << 20):                                          # short, right or long: still right
+    for hint in (max(1, max(lens)), 1 << 20):
         c.check(*c.run(pq, max_len=hint))
+    for most in (1, 130, 700):                                              # longer sequences count as max_len
+        got = c.run(pq, max_len=most)
+        full, c.lens = c.lens, [min(n, most) for n in c.lens]
+        c.check(*got)
+        c.lens = full
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
@@ -337,3 +342,20 @@ def test_without_workspace_on_another_stream(pq):
     pq.pq_attn_decode(c.cache, q, table, lens, out, stream=side)
     side.synchronize()
     assert torch.equal(out.cpu(), want)
+
+
+def test_one_workspace_for_calls_of_other_sizes(pq):
+    """Calls in a row on one stream with one workspace: long and split, short, long again."""
+    cases = [Case(pq, f, lens, 2, 4, 64, 16, torch.bfloat16, seed=i)
+             for i, (f, lens) in enumerate([("kv8", [6000, 40]), ("kv4", [3]), ("kv16", [4000]), ("kv8", [0, 900, 2])])]
+    ws = pq.attn_workspace(cases[0].cache, 3, 8)
+    outs = []
+    for c in cases * 2:
+        b = len(c.lens)
+        out, lse = torch.empty(b, 8, 64, dtype=torch.bfloat16, device=DEV), torch.empty(b, 8, device=DEV)
+        pq.pq_attn_decode(c.cache, c.q.to(DEV), c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV), out, lse,
+                          workspace=ws)
+        outs.append((c, out, lse))
+    torch.cuda.synchronize()
+    for c, out, lse in outs:
+        c.check(out.cpu(), lse.cpu())

@@ -117,7 +117,7 @@ def test_workspace_size(pq):
     c = cache(pq)
     q = lambda b, h: pq.lib.pq_attn_decode_workspace_bytes(ctypes.addressof(c), b, h)  # noqa: E731
     assert q(0, 8) == 0 and q(1, 6) == -1 and q(-1, 8) == -1 and q(1, 0) == -1
-    assert q(1, 8) == q(64, 8) > 0 and q(1, 8) % 16 == 0
+    assert q(64, 8) >= q(1, 8) > 0 and q(1, 8) % 16 == 0
     a = attn_args(pq, c)
     a[19] = q(2, 8) - 16
     assert pq.lib.pq_attn_decode(*a) == 7
