@@ -33,8 +33,9 @@
 // works on tokens of its own: the softmax costs 1 / R.
 //
 // Work split.  The cache is read once and every byte costs the same, so the
-// steps of all (sequence, head) rows are laid end to end and cut into equal
-// shares, one per block, whatever the lengths are.  A row that lies in one
+// steps of all (sequence, head) rows, each row with kRowCost more for its
+// beginning and end, are laid end to end and cut into equal shares, one per
+// block, whatever the lengths are.  A row that lies in one
 // share is written directly; of the others each share leaves (m, l, o) in the
 // workspace, and a second kernel joins them, in order.  Short rows are not
 // split: one block each and no second kernel.
@@ -43,6 +44,7 @@
 #include <stdint.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "pq_kv_common.hpp"
 
@@ -57,6 +59,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 constexpr int kMaxBatch = 1024;     // sequences of one launch (their step counts sit in LDS)
 constexpr int kMaxShares = 512;     // blocks of one launch: two per CU
 constexpr int kWaves = 4;
+// What a row costs a share beyond its steps (first loads, joining the waves,
+// a last round with idle waves), in steps of one wave.
+constexpr int kRowCost = 8;
 
 struct AttnArgs {
     const uint8_t *k, *v;
@@ -101,15 +106,15 @@ __device__ __forceinline__ Range range_of(const AttnArgs &a, int len)
     return r;
 }
 
-// lens[i] = clamped lengths; pre[i] = steps of sequences before i, pre[batch]
-// their sum; 256 threads.
+// lens[i] = clamped lengths; pre[i] = steps and row costs of one head of the
+// sequences before i, pre[batch] their sum; 256 threads.
 __device__ __forceinline__ void step_prefix(const AttnArgs &a, int unit, int *lens, int *pre, int *wave_sum)
 {
     int before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 256) {
         const int b = b0 + static_cast<int>(threadIdx.x);
         const Range r = range_of(a, b < a.batch ? a.lens[b] : 0);
-        const int n = r.steps(unit);
+        const int n = r.len > r.first ? r.steps(unit) + kRowCost : 0;
         int s = n;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -133,8 +138,8 @@ __device__ __forceinline__ void step_prefix(const AttnArgs &a, int unit, int *le
     __syncthreads();
 }
 
-// The cut into shares: the first `more` shares have `each` + 1 steps, the
-// others `each`.
+// The cut of the line of steps and row costs into shares: the first `more`
+// have `each` + 1 of them, the others `each`.
 struct Cut {
     int each, more;
     __device__ __forceinline__ int begin(int share) const { return share * each + min(share, more); }
@@ -143,8 +148,8 @@ struct Cut {
         const int wide = more * (each + 1);
         return step < wide ? step / (each + 1) : more + (step - wide) / each;
     }
-    // Which partial a share writes for the row that starts at step `row0`:
-    // that of the row it begins in, or that of the row it ends in.
+    // Which partial a share writes for the row that starts at `row0`: that of
+    // the row it begins in, or that of the row it ends in.
     __device__ __forceinline__ int slot(int share, int row0) const { return 2 * share + (row0 > begin(share) ? 1 : 0); }
 };
 
@@ -158,6 +163,16 @@ __device__ __forceinline__ float column_sum(float x)
 {
     x += __shfl_xor(x, 16);
     return x + __shfl_xor(x, 32);
+}
+
+// A wave-uniform address in scalar registers, its sum closed to the compiler:
+// it would else add the lane's offset to the base first and spend a 64-bit
+// vector addition per load.
+__device__ __forceinline__ const PQ_GLOBAL uint8_t *scalar_address(const uint8_t *p)
+{
+    uint64_t u = reinterpret_cast<uint64_t>(p);
+    asm("" : "+s"(u));
+    return reinterpret_cast<const PQ_GLOBAL uint8_t *>(u);
 }
 
 template <bool F16>
@@ -281,46 +296,60 @@ struct Attn {
         for (int e = 0; e < E; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Rows of the 16 tokens at `row` (wave-uniform).  Channels past dim: any,
-    // q is 0 there.
-    __device__ __forceinline__ void load_k(const AttnArgs &a, int r, int tile, const uint8_t *row)
+    // Byte offsets of the lane's loads from a 16-token tile's first row; with
+    // the tile's wave-uniform address they are the hardware's base + 32-bit
+    // offset form.  Channels past dim: any, q is 0 there.
+    uint32_t k_off, k_last, v_off, v_step;
+
+    __device__ __forceinline__ void set_offsets(const AttnArgs &a)
     {
-        const uint8_t *p = row + column() * a.token_stride;
+        const uint32_t row = column() * a.token_stride;
+        // run c of K lies 16 * 4 (4-bit: 8 * 4) bytes after run c - 1, the last one inside the row
+        const uint32_t run = KW * 4, row_bytes = kRaw ? 2 * a.dim : FMT == PQ_KV_8 ? a.dim : a.dim / 2;
+        k_off = row + kb() * run;
+        k_last = row + row_bytes - run;
+        const uint32_t d = min(column() * E, a.dim - E);
+        v_off = 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
+        v_step = a.token_stride;
+    }
+
+    __device__ __forceinline__ void load_k(int r, int tile, const uint8_t *tile_row)
+    {
+        const PQ_GLOBAL uint8_t *row = scalar_address(tile_row);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
+            const uint32_t at = min(k_off + c * (KW * 16), k_last);
             if constexpr (KW == 2) {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(p + min(32 * c + 8 * kb(), a.dim / 2 - 8));
+                const u32x2 w = *reinterpret_cast<const PQ_GLOBAL u32x2 *>(row + at);
                 k[r][tile][c][0] = w[0];
                 k[r][tile][c][1] = w[1];
             } else {
-                const int at = kRaw ? 2 * min(32 * c + 8 * kb(), a.dim - 8) : min(64 * c + 16 * kb(), a.dim - 16);
-                const u32x4 w = *reinterpret_cast<const u32x4_a8 *>(p + at);
+                const u32x4 w = *reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(row + at);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) k[r][tile][c][e] = w[e];
             }
         }
     }
 
-    __device__ __forceinline__ void load_v(const AttnArgs &a, int r, int tile, const uint8_t *row)
+    __device__ __forceinline__ void load_v(int r, int tile, const uint8_t *tile_row)
     {
-        const int d = min(column() * E, a.dim - E);
-        const uint8_t *p = row + 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
+        const PQ_GLOBAL uint8_t *row = scalar_address(tile_row);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t *t = p + j * a.token_stride;
+            const PQ_GLOBAL uint8_t *t = row + (v_off + j * v_step);
             uint32_t(&w)[VW] = v[r][tile][j];
             if constexpr (FMT == PQ_KV_4 && E == 4) {
-                w[0] = *reinterpret_cast<const uint16_t *>(t);
+                w[0] = *reinterpret_cast<const PQ_GLOBAL uint16_t *>(t);
             } else if constexpr (VW == 1) {
-                w[0] = *reinterpret_cast<const uint32_t *>(t);
+                w[0] = *reinterpret_cast<const PQ_GLOBAL uint32_t *>(t);
             } else if constexpr (VW == 2) {
-                const u32x2 x = *reinterpret_cast<const u32x2 *>(t);
+                const u32x2 x = *reinterpret_cast<const PQ_GLOBAL u32x2 *>(t);
                 w[0] = x[0];
                 w[1] = x[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < VW / 4; ++i) {
-                    const u32x4 x = reinterpret_cast<const u32x4_a8 *>(t)[i];
+                    const u32x4 x = reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(t)[i];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
                 }
@@ -413,6 +442,7 @@ struct Attn {
             }
         }
         if (masked) {
+            asm volatile("");                       // a branch: not selects in every step
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const bool on = seen >> i & 1;
@@ -473,11 +503,17 @@ struct Attn {
                     w[i] = own ? lo[i] : 0u;
                 }
             }
+            // four channels at a time, so that no product waits for the one before
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const u32x4 f = v_operand(r, e);
-                o[e] = mfma16<kF16>(f, h, o[e]);
-                o[e] = mfma16<kF16>(f, w, o[e]);
+            for (int e0 = 0; e0 < E; e0 += 4) {
+                u32x4 f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[e] = v_operand(r, e0 + e);
+                    o[e0 + e] = mfma16<kF16>(f[e], h, o[e0 + e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e0 + e] = mfma16<kF16>(f[e], w, o[e0 + e]);
             }
         }
     }
@@ -506,7 +542,8 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, int b, int hq, int 
 // A row (sequence, cache head, head tile) of a share, as its waves see it.
 struct Row {
     int b, kvh, gt;
-    int row0, n, stop;              // its first step, its steps; where the share's part of it ends
+    int row0, n;                    // its beginning on the line, and its length there: kRowCost, then its steps
+    int step0, stop;                // the share's part: its first step; where it ends on the line
     Range r;
     int t0, count;                  // the wave's first token; its steps (every kWaves-th)
 };
@@ -537,7 +574,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
     }
     const int in_page = (1 << a.page_log2) - 1;
 
-    auto row_of = [&](int at, int b) {              // the row of step `at`, in sequence b or later
+    auto row_of = [&](int at, int b) {              // the row at `at`, in sequence b or later
         Row w;
         while (s_pre[b + 1] * vheads <= at) ++b;    // also past sequences without steps
         w.b = __builtin_amdgcn_readfirstlane(b);
@@ -549,55 +586,71 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         w.gt = vh - w.kvh * a.gtiles;
         w.stop = min(w.row0 + w.n, end);
         w.r = range_of(a, __builtin_amdgcn_readfirstlane(s_len[w.b]));
-        w.t0 = w.r.base + (at - w.row0 + wave) * kUnit;
-        w.count = (w.stop - at - wave + kWaves - 1) / kWaves;
+        w.step0 = max(at - w.row0 - kRowCost, 0);
+        w.t0 = w.r.base + (w.step0 + wave) * kUnit;
+        w.count = max(w.stop - w.row0 - kRowCost - w.step0 - wave + kWaves - 1, 0) / kWaves;
         return w;
     };
-    auto load_ids = [&](const Row &w, int i0) {     // page ids of steps i0 .. i0 + kBatch - 1, one a lane
+    // Page ids of steps i0 .. i0 + kBatch - 1, one a lane; -1 where there is
+    // none.  Nothing looks at the loaded value here, so that the wave does not
+    // wait for it.
+    auto load_ids = [&](const Row &w, int i0) {
         const int i = i0 + lane / kIds;
         const int t = w.t0 + i * (kWaves * kUnit) + lane % kIds * 16;
         int id = -1;
-        if (i < w.count && t < w.r.len) {
-            id = a.table[w.b * a.table_stride + (t >> a.page_log2)];
-            if (id < 0 || id >= a.num_pages) id = -1;
-        }
+        if (i < w.count && t < w.r.len) id = a.table[w.b * a.table_stride + (t >> a.page_log2)];
         return id;
     };
+    // A step whose loads are under way or wanted: its tiles' page ids, in
+    // scalar registers.
+    struct Step {
+        int id[kIds], t;            // t: the wave's first token in it
+    };
+    auto step_at = [&](const Row &w, int held, int i) {
+        Step f;
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) f.id[k] = __builtin_amdgcn_readlane(held, (i % kBatch) * kIds + k);
+        f.t = w.t0 + i * (kWaves * kUnit);
+        return f;
+    };
+    const int pages = static_cast<int>(a.num_pages);
+    auto valid = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(pages); };
     A st;
+    st.set_offsets(a);
+    int64_t tile_at[kIds];                          // byte offsets of a step's tiles in k and v
     // hidden tiles are read from page 0 and masked
-    auto row_at = [&](const Row &w, int held, int i, int tile) {
-        const int id = max(__builtin_amdgcn_readlane(held, (i % kBatch) * kIds + tile), 0);
-        const int off = (w.t0 + i * (kWaves * kUnit) + tile * 16) & in_page;
-        return id * a.page_stride + w.kvh * a.head_stride + static_cast<int64_t>(off) * a.token_stride;
-    };
-    auto load_keys = [&](const Row &w, int held, int i) {
+    auto load_keys = [&](int kvh, const Step &f) {
 #pragma unroll
-        for (int t = 0; t < kIds; ++t) st.load_k(a, t >> 1, t & 1, a.k + row_at(w, held, i, t));
+        for (int t = 0; t < kIds; ++t) {
+            const int off = (f.t + t * 16) & in_page;
+            tile_at[t] = (valid(f.id[t]) ? f.id[t] : 0) * a.page_stride + kvh * a.head_stride +
+                         static_cast<int64_t>(off) * a.token_stride;
+            st.load_k(t >> 1, t & 1, a.k + tile_at[t]);
+        }
     };
-    auto load_values = [&](const Row &w, int held, int i) {
+    auto load_values = [&]() {                      // of the step whose keys were loaded last
 #pragma unroll
-        for (int t = 0; t < kIds; ++t) st.load_v(a, t >> 1, t & 1, a.v + row_at(w, held, i, t));
+        for (int t = 0; t < kIds; ++t) st.load_v(t >> 1, t & 1, a.v + tile_at[t]);
     };
-    auto load_pairs = [&](const Row &w, int held, int i) {
+    auto load_pairs = [&](int kvh, const Step &f) {
         if constexpr (!A::kRaw) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int tile = 2 * A::copy() + t;
-                const int id = max(__shfl(held, (i % kBatch) * kIds + tile), 0);
-                const int off = (w.t0 + i * (kWaves * kUnit) + tile * 16) & in_page;
-                const int64_t p = ((static_cast<int64_t>(id) * a.heads + w.kvh) << a.page_log2) + off + 4 * kb;
+                int64_t at[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int id = f.id[2 * r + t];
+                    at[r] = ((static_cast<int64_t>(valid(id) ? id : 0) * a.heads + kvh) << a.page_log2) +
+                            ((f.t + (2 * r + t) * 16) & in_page);
+                }
+                int64_t p = at[0];
+#pragma unroll
+                for (int r = 1; r < R; ++r) p = A::copy() == r ? at[r] : p;
+                p += 4 * kb;
                 st.kpar[t] = *reinterpret_cast<const u32x4 *>(a.kp + p);
                 st.vpar[t] = *reinterpret_cast<const u32x4 *>(a.vp + p);
             }
         }
-    };
-    auto start = [&](const Row &w, int held) {      // first loads of a row
-        if (w.count > 0) {
-            load_keys(w, held, 0);
-            load_pairs(w, held, 0);
-            load_values(w, held, 0);
-        }
-        st.load_q(a, w.b, w.kvh, w.gt);
     };
 
     Row w;
@@ -609,58 +662,96 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
             else hi = mid - 1;
         }
         w = row_of(begin, b0);
+        if (w.stop <= w.row0 + kRowCost) return;    // none of its steps
     } else {                                        // the block's own row
         w.b = blockIdx.x / vheads;
         const int vh = blockIdx.x - w.b * vheads;
         w.kvh = vh / a.gtiles;
         w.gt = vh - w.kvh * a.gtiles;
         w.r = range_of(a, a.lens[w.b]);
-        w.row0 = 0;
-        w.n = w.stop = end = w.r.steps(kUnit);
+        w.row0 = w.step0 = 0;
+        w.n = w.stop = end = w.r.steps(kUnit) + kRowCost;
         w.t0 = w.r.base + wave * kUnit;
-        w.count = (w.n - wave + kWaves - 1) / kWaves;
+        w.count = max(w.n - kRowCost - wave + kWaves - 1, 0) / kWaves;
     }
-    int ids = load_ids(w, 0);
-    start(w, ids);
+    // Loads run one step ahead: a step's keys, pairs and values are asked for as
+    // soon as the step before has used its own, the first ones of a row during
+    // the last step of the row before.  They are never under a branch inside a
+    // step (a step without a successor asks for its own data again): with one
+    // the compiler can only wait for all of them.
+    bool ready = false;                             // the row's first loads are under way
+    int held = load_ids(w, 0);
     for (;;) {
-        st.set_q(a);
-        st.clear();
-        // the next row's page ids come along with this row
-        const bool follows = w.stop < end;
+        const bool follows = w.stop + kRowCost < end;       // with a step of it at least
         Row next = w;
-        int next_ids = -1;
+        int next_held = -1;
         if (follows) {
             next = row_of(w.stop, w.b);
-            next_ids = load_ids(next, 0);
+            next_held = load_ids(next, 0);
         }
-        int ids_after = ids;
+        Step now = step_at(w, held, 0);
+        if (!ready) {
+            st.load_q(a, w.b, w.kvh, w.gt);
+            if (w.count > 0) {
+                load_keys(w.kvh, now);
+                load_values();
+                load_pairs(w.kvh, now);
+            }
+        }
+        asm volatile("" : "+v"(next_held));         // arrived before the steps begin
+        st.set_q(a);
+        st.clear();
+        int held_after = -1;
+        // Two blocks share a CU, and its older waves go first: a priority that
+        // falls with each quarter of the share keeps the two level (3 % of 64
+        // ragged 4-bit contexts).
+        const int quarter = (end - begin + 3) >> 2;
         for (int i = 0; i < w.count; ++i) {
-            if (i % kBatch == 0 && i + kBatch < w.count) ids_after = load_ids(w, i + kBatch);
+            const int done = w.row0 + kRowCost + w.step0 + i * kWaves - begin;
+            if (done >= 3 * quarter) __builtin_amdgcn_s_setprio(0);
+            else if (done >= 2 * quarter) __builtin_amdgcn_s_setprio(1);
+            else if (done >= quarter) __builtin_amdgcn_s_setprio(2);
+            else __builtin_amdgcn_s_setprio(3);
             float x[8];
             st.first_product(x);
-            const int here = ids;
-            if ((i + 1) % kBatch == 0) ids = ids_after;
-            const bool more = i + 1 < w.count;
-            if (more) load_keys(w, ids, i + 1);
-            const int own = 2 * A::copy(), t = w.t0 + i * (kWaves * kUnit);
-            const int id_a = __shfl(here, (i % kBatch) * kIds + own), id_b = __shfl(here, (i % kBatch) * kIds + own + 1);
-            const bool masked = __ballot(id_a < 0 || id_b < 0) != 0 || t < w.r.first || t + kUnit > w.r.len;
+            if (i % kBatch == 0 && i + kBatch < w.count) held_after = load_ids(w, i + kBatch);
+            Step then = now;
+            int kvh = w.kvh;
+            if (i + 1 < w.count) {
+                if ((i + 1) % kBatch == 0) {
+                    asm volatile("" : "+v"(held_after));
+                    held = held_after;
+                }
+                then = step_at(w, held, i + 1);
+            } else if (follows && next.count > 0) {
+                then = step_at(next, next_held, 0);
+                kvh = next.kvh;
+            }
+            load_keys(kvh, then);
+            bool masked = now.t < w.r.first || now.t + kUnit > w.r.len;
+#pragma unroll
+            for (int k = 0; k < kIds; ++k) masked = masked || !valid(now.id[k]);
             unsigned seen = 0xFF;
             if (masked) {
                 seen = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int u = t + own * 16 + 4 * kb + (e >> 2) * 16 + (e & 3);
-                    if ((e < 4 ? id_a : id_b) >= 0 && u >= w.r.first && u < w.r.len) seen |= 1u << e;
+                    int id = now.id[e >> 2];
+#pragma unroll
+                    for (int r = 1; r < R; ++r) id = A::copy() == r ? now.id[2 * r + (e >> 2)] : id;
+                    const int u = now.t + A::copy() * 32 + 4 * kb + (e >> 2) * 16 + (e & 3);
+                    if (valid(id) && u >= w.r.first && u < w.r.len) seen |= 1u << e;
                 }
             }
             u32x4 hi, lo;
             st.softmax(x, seen, masked, hi, lo);
-            if (more) load_pairs(w, ids, i + 1);
+            load_pairs(kvh, then);
             st.second_product(hi, lo);
-            if (more) load_values(w, ids, i + 1);
+            load_values();
+            now = then;
         }
-        if (follows) start(next, next_ids);         // its loads pass while this row is joined
+        if (w.count > 0 && follows) st.load_q(a, next.b, next.kvh, next.gt);
+        ready = w.count > 0 && follows && next.count > 0;
         // join the waves and the copies of the columns
         const float l_all = column_sum(st.l), z_all = column_sum(st.zsum);
         __syncthreads();                            // the last row's s_m and s_o have been read
@@ -691,7 +782,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
                               st.o[e + 2][i] * (f * A::o_unit(0)), st.o[e + 3][i] * (f * A::o_unit(1))};
         }
         __syncthreads();
-        const bool whole = w.row0 >= begin && w.row0 + w.n <= end;
+        const bool opens = w.row0 + kRowCost >= begin, whole = opens && w.row0 + w.n <= end;
         const int slot = cut.slot(blockIdx.x, w.row0), hq0 = w.kvh * a.group + w.gt * 16;
         for (int i = tid * 4; i < rows * DP; i += 1024) {
             const int g = i / DP, d = i - g * DP;
@@ -717,12 +808,12 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
                 if (d == 0) a.part_ml[at] = f32x2{M - A::kShift, L};
             }
         }
-        if (a.shares && w.row0 >= begin && tid == 0)        // for the join: whose partials make up the row
+        if (a.shares && opens && tid == 0)          // for the join: whose partials make up the row
             a.spans[(w.b * a.heads + w.kvh) * a.gtiles + w.gt] =
                 make_int2(slot, cut.share_of(w.row0 + w.n - 1));
         if (!follows) break;
         w = next;
-        ids = next_ids;
+        held = next_held;
     }
 }
 
@@ -924,8 +1015,8 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     if (max_len > 0 && max_len < a.max_tokens) a.max_tokens = static_cast<int>(max_len);
     int64_t longest = a.max_tokens;
     if (window > 0 && longest > window + 15) longest = window + 15;   // its first tile may start 15 tokens early
-    // the kernel counts steps of at least 32 tokens in 32 bits
-    const int64_t row_steps = (static_cast<int64_t>(a.max_tokens) + 31) / 32 + 1;
+    // the kernel counts steps of at least 32 tokens and row costs in 32 bits
+    const int64_t row_steps = (static_cast<int64_t>(a.max_tokens) + 31) / 32 + 1 + kRowCost;
     int64_t most = INT32_MAX / (row_steps * c.heads * a.gtiles);
     if (most < 1) return PQ_ERR_SHAPE;
     if (most > kMaxBatch) most = kMaxBatch;
