@@ -184,9 +184,24 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+// 16 and 8 bytes at a multiple of 8.
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const PQ_GLOBAL uint8_t *p)
+{
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(p));
+    else return *reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(p);
+}
+template <bool NT>
+__device__ __forceinline__ u32x2 load8(const PQ_GLOBAL uint8_t *p)
+{
+    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const PQ_GLOBAL u32x2 *>(p));
+    else return *reinterpret_cast<const PQ_GLOBAL u32x2 *>(p);
+}
+
 // QT: type of q and out (and of a 16-bit cache).  FMT: cache format.  DP: dim
-// rounded up to 64, 128 or 256.  R: copies of the heads in the columns.
-template <typename QT, int FMT, int DP, int R>
+// rounded up to 64, 128 or 256.  R: copies of the heads in the columns.  NT:
+// the cache is read past the caches (launch_one).
+template <typename QT, int FMT, int DP, int R, bool NT>
 struct Attn {
     static constexpr bool kRaw = FMT == PQ_KV_16;
     static constexpr bool kF16 = !kRaw || __is_same(QT, f16_t);   // operand type of both products
@@ -198,7 +213,8 @@ struct Attn {
     static constexpr int kUnit = 32 * R;    // tokens of a step
     static constexpr int kCols = 16 / R;    // heads of a tile
     static constexpr int KS = DP / 32;      // k steps of the first product
-    static constexpr int E = DP / 16;       // channels of a lane in the second
+    static constexpr int E = DP / 16;       // channels of a lane in the second, in runs of kRun
+    static constexpr int kRun = kRaw && E == 16 ? 8 : E;    // (one 16-byte load each, side by side over the lanes)
     // Words of a lane per 16 tokens: K in KC runs of KW words (16-bit rows: 8
     // channels of step s at 32 s + 8 kb; codes: 16 channels at 64 c + 16 kb,
     // which are steps 2c and 2c + 1), V in VW words per token.
@@ -299,7 +315,7 @@ struct Attn {
     // Byte offsets of the lane's loads from a 16-token tile's first row; with
     // the tile's wave-uniform address they are the hardware's base + 32-bit
     // offset form.  Channels past dim: any, q is 0 there.
-    uint32_t k_off, k_last, v_off, v_step;
+    uint32_t k_off, k_last, v_off, v_step, v_second;
 
     __device__ __forceinline__ void set_offsets(const AttnArgs &a)
     {
@@ -308,7 +324,8 @@ struct Attn {
         const uint32_t run = KW * 4, row_bytes = kRaw ? 2 * a.dim : FMT == PQ_KV_8 ? a.dim : a.dim / 2;
         k_off = row + kb() * run;
         k_last = row + row_bytes - run;
-        const uint32_t d = min(column() * E, a.dim - E);
+        const uint32_t d = min(column() * kRun, a.dim - kRun);
+        v_second = 2 * (min(128u + column() * kRun, static_cast<uint32_t>(a.dim - kRun)) - d);
         v_off = 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
         v_step = a.token_stride;
     }
@@ -324,7 +341,7 @@ struct Attn {
                 k[r][tile][c][0] = w[0];
                 k[r][tile][c][1] = w[1];
             } else {
-                const u32x4 w = *reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(row + at);
+                const u32x4 w = load16<NT>(row + at);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) k[r][tile][c][e] = w[e];
             }
@@ -343,13 +360,14 @@ struct Attn {
             } else if constexpr (VW == 1) {
                 w[0] = *reinterpret_cast<const PQ_GLOBAL uint32_t *>(t);
             } else if constexpr (VW == 2) {
-                const u32x2 x = *reinterpret_cast<const PQ_GLOBAL u32x2 *>(t);
+                const u32x2 x = load8<NT>(t);
                 w[0] = x[0];
                 w[1] = x[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < VW / 4; ++i) {
-                    const u32x4 x = reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(t)[i];
+                    // a second run (16-bit rows of over 128 channels) lies 128 channels on
+                    const u32x4 x = load16<NT>(i ? t + v_second : t);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
                 }
@@ -386,7 +404,7 @@ struct Attn {
         return c;
     }
 
-    // Operand of channel E * column + e: tokens 4 kb + j of the block's first tile, then of its second.
+    // Operand of channel(column, e): tokens 4 kb + j of the block's first tile, then of its second.
     __device__ __forceinline__ u32x4 v_operand(int r, int e) const
     {
         u32x4 f;
@@ -518,6 +536,9 @@ struct Attn {
         }
     }
 
+    // The channel that element e of a lane in row n (column n of V) stands for.
+    static __device__ __forceinline__ int channel(int n, int e) { return e / kRun * 128 + kRun * n + e % kRun; }
+
     // What a unit of o[e] stands for.
     static __device__ __forceinline__ float o_unit(int e)
     {
@@ -548,10 +569,10 @@ struct Row {
     int t0, count;                  // the wave's first token; its steps (every kWaves-th)
 };
 
-template <typename QT, int FMT, int DP, int R>
+template <typename QT, int FMT, int DP, int R, bool NT>
 __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs a)
 {
-    using A = Attn<QT, FMT, DP, R>;
+    using A = Attn<QT, FMT, DP, R, NT>;
     constexpr int E = A::E, kUnit = A::kUnit, kCols = A::kCols;
     constexpr int kPad = DP + 4;
     constexpr int kIds = 2 * R, kBatch = 64 / kIds;         // page ids of a step; steps whose ids a wave holds
@@ -777,7 +798,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int e = 0; e < E; e += 4)
-                    *reinterpret_cast<f32x4 *>(so + E * (4 * kb + i) + e) =
+                    *reinterpret_cast<f32x4 *>(so + A::channel(4 * kb + i, e)) =
                         f32x4{st.o[e][i] * (f * A::o_unit(0)), st.o[e + 1][i] * (f * A::o_unit(1)),
                               st.o[e + 2][i] * (f * A::o_unit(0)), st.o[e + 3][i] * (f * A::o_unit(1))};
         }
@@ -891,20 +912,40 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
 // in kWholeRow / 128 rounds, and a second launch would cost more.
 constexpr int kWholeRow = 512;
 
-template <typename QT, int FMT, int DP, int R>
+// A call whose cache is larger than the memory-side cache (256 MB) finds
+// nothing of it there: its loads are non-temporal then (32 contexts of 16 Ki
+// bf16 tokens, 1.9 GB: 297 us against 326), but only where a row is whole
+// 128-byte lines, else lines that two loads share are fetched twice (bf16 rows
+// of 80 channels: 108 us against 85).  A smaller cache may still lie there
+// from the call before (16 chats, 67 MB: 21 us against 17.5).
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+
+template <typename QT, int FMT, int DP, int R, bool NT>
 void launch_one(AttnArgs a, int64_t longest, hipStream_t s)
 {
     const int unit = 32 * R;
     const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * a.gtiles;
     if (longest <= kWholeRow) {
         a.shares = 0;
-        hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R, NT>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
         return;
     }
     const int64_t want = (rows * ((longest + unit - 1) / unit) + kWaves - 1) / kWaves;    // a step per wave at least
     a.shares = static_cast<int>(want > kMaxShares ? kMaxShares : want);
-    hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R>), dim3(static_cast<unsigned>(a.shares)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R, NT>), dim3(static_cast<unsigned>(a.shares)), dim3(256), 0, s, a);
     hipLaunchKernelGGL(k_attn_join<QT>, dim3(static_cast<unsigned>(a.batch * a.q_heads)), dim3(256), 0, s, a);
+}
+
+template <typename QT, int FMT, int DP, int R>
+void launch_stream(const AttnArgs &a, int64_t longest, hipStream_t s)
+{
+    constexpr int kRow = FMT == PQ_KV_16 ? 2 * DP : DP;     // bytes of a full row
+    constexpr int kHeld = 2 * (kRow + (FMT == PQ_KV_16 ? 0 : 4));
+    if constexpr (FMT != PQ_KV_4 && kRow % 128 == 0) {
+        if (a.dim == DP && longest * a.batch * a.heads * kHeld > kStreamBytes && a.token_stride % 128 == 0)
+            return launch_one<QT, FMT, DP, R, true>(a, longest, s);
+    }
+    launch_one<QT, FMT, DP, R, false>(a, longest, s);
 }
 
 template <typename QT, int FMT, int DP>
@@ -913,9 +954,9 @@ void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
     // Two copies of the heads in the columns where the group leaves room.
     // 16-bit rows take none: their bytes outlast the softmax.
     if constexpr (FMT != PQ_KV_16) {
-        if (a.group <= 8) return launch_one<QT, FMT, DP, 2>(a, longest, s);
+        if (a.group <= 8) return launch_stream<QT, FMT, DP, 2>(a, longest, s);
     }
-    launch_one<QT, FMT, DP, 1>(a, longest, s);
+    launch_stream<QT, FMT, DP, 1>(a, longest, s);
 }
 
 template <typename QT, int FMT>

@@ -359,3 +359,17 @@ def test_one_workspace_for_calls_of_other_sizes(pq):
     torch.cuda.synchronize()
     for c, out, lse in outs:
         c.check(out.cpu(), lse.cpu())
+
+
+@pytest.mark.parametrize("fmt,dim", [("kv16", 64), ("kv16", 128), ("kv16", 256), ("kv8", 128), ("kv8", 256)])
+@pytest.mark.parametrize("group", [4, 12])
+def test_large_caches_are_streamed(pq, fmt, dim, group):
+    """A page table that allows over 256 MB of cache takes the reads past the caches."""
+    c = Case(pq, fmt, [0, 700, 33, 129], 2, group, dim, 64, torch.bfloat16, seed=dim)
+    want = c.run(pq)
+    wide = torch.full((4, 1 << 13), -1, dtype=torch.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    out, lse = c.run(pq)
+    c.check(out, lse)
+    c.check(*want)
