@@ -22,6 +22,10 @@ namespace {
 
 // ------------------------------------------------------------------ append
 
+// Row groups a wave has in flight: one, and six waves per SIMD (14 Ki tokens of
+// 30 heads of 80 channels 38 us; two groups 40, four 47).
+constexpr int kAppendRows = 1;
+
 struct AppendArgs {
     uint8_t *k, *v;
     uint32_t *kp, *vp;
@@ -36,7 +40,7 @@ struct AppendArgs {
     int64_t tokens;
     int max_pos, rot, half, q_heads;
     int lanes_log2;                 // log2 of the lanes of a row (8 channels each)
-    int rows, slices;               // rows of a token (2 heads + q_heads); waves per token
+    int groups, slices;             // row groups of a token (K, V, Q); waves per token
 };
 
 // The rotation of one lane's 8 channels d0 .. d0 + 7: y = x c + partner s per
@@ -44,20 +48,17 @@ struct AppendArgs {
 // rotated channel.
 struct Turn {
     float c[8], s[8];
-    int partner;                    // half layout: channel of element 0's partner
     unsigned on;
 };
 
 __device__ __forceinline__ void load_turn(const AppendArgs &a, int d0, int pos, Turn &t)
 {
     t.on = 0;
-    t.partner = d0;
     if (!a.table || pos < 0 || d0 >= a.rot) return;
     const int hr = a.rot / 2;
     const bool known = pos < a.max_pos;
     const float *row = a.table + static_cast<int64_t>(known ? pos : 0) * a.rot;
     const bool whole = a.rot % 16 == 0;             // a lane's channels and their partners are whole 8-channel runs
-    t.partner = d0 < hr ? d0 + hr : d0 - hr;
     if (whole) {
         float cs[16];
         const int first = a.half ? (d0 < hr ? d0 : d0 - hr) : d0 / 2;
@@ -93,9 +94,11 @@ __device__ __forceinline__ void load_turn(const AppendArgs &a, int d0, int pos, 
     }
 }
 
-// x: the lane's channels of a row, already loaded; `row` points at the row.
+// x: the lane's channels of a row; `other`: its partner's run (half layout,
+// whole runs); `row` points at the row.
 template <typename T>
-__device__ __forceinline__ void apply_turn(const AppendArgs &a, const Turn &t, const T *row, int d0, float (&x)[8])
+__device__ __forceinline__ void apply_turn(const AppendArgs &a, const Turn &t, const Raw8<T> &other, const T *row, int d0,
+                                           float (&x)[8])
 {
     if (!t.on) return;
     float y[8];
@@ -103,7 +106,7 @@ __device__ __forceinline__ void apply_turn(const AppendArgs &a, const Turn &t, c
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
     } else if (a.rot % 16 == 0) {
-        load_f32<T, 8>(row + t.partner, y);
+        raw_to_f32<T>(other, y);
     } else {
         const int hr = a.rot / 2;
 #pragma unroll
@@ -112,105 +115,171 @@ __device__ __forceinline__ void apply_turn(const AppendArgs &a, const Turn &t, c
             y[e] = d < a.rot ? to_f32(row[d < hr ? d + hr : d - hr]) : 0.f;
         }
     }
+    if (t.on == 0xFF) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (t.on >> e & 1) x[e] = x[e] * t.c[e] + y[e] * t.s[e];
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * t.c[e] + y[e] * t.s[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (t.on >> e & 1) x[e] = x[e] * t.c[e] + y[e] * t.s[e];
+    }
 }
 
 // Minimum and maximum that keep a NaN.
 __device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
-// One wave per token and slice of its rows: 2 heads rows of K and V, then the
-// query heads.  2^lanes_log2 lanes hold a row, 8 channels each, so the row's
-// minimum and maximum are a butterfly inside them and a wave takes several
-// rows at once; the rotation's table values stay in registers over the rows.
+// Minimum and maximum over the 2^l lanes of a row: neighbours, pairs, quads and
+// eights exchange by DPP (mirrors serve, since the lanes of a half agree).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ void row_range(int l, float &mn, float &mx)
+{
+    constexpr int kPairs = 0xB1, kQuads = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm 1 0 3 2; 2 3 0 1
+    mn = min_nan(mn, dpp<kPairs>(mn));
+    mx = max_nan(mx, dpp<kPairs>(mx));
+    if (l >= 2) {
+        mn = min_nan(mn, dpp<kQuads>(mn));
+        mx = max_nan(mx, dpp<kQuads>(mx));
+    }
+    if (l >= 3) {
+        mn = min_nan(mn, dpp<kHalfMirror>(mn));
+        mx = max_nan(mx, dpp<kHalfMirror>(mx));
+    }
+    if (l >= 4) {
+        mn = min_nan(mn, dpp<kMirror>(mn));
+        mx = max_nan(mx, dpp<kMirror>(mx));
+    }
+    if (l >= 5) {
+        mn = min_nan(mn, __shfl_xor(mn, 16));
+        mx = max_nan(mx, __shfl_xor(mx, 16));
+    }
+}
+
+// Codes of a lane's 8 channels, as they lie in the row: whole numbers in fp32,
+// put together two or four at a time by exact multiply-adds.
+template <int FMT>
+__device__ __forceinline__ u32x2 pack_codes(const float (&n)[8])
+{
+    u32x2 w;
+    if constexpr (FMT == PQ_KV_8) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = static_cast<uint32_t>(__builtin_fmaf(n[4 * i + 1], 256.f, n[4 * i]));
+            const uint32_t hi = static_cast<uint32_t>(__builtin_fmaf(n[4 * i + 3], 256.f, n[4 * i + 2]));
+            w[i] = hi << 16 | lo;
+        }
+    } else {
+        uint32_t h[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float lo = __builtin_fmaf(n[4 * i + 1], 16.f, n[4 * i]), hi = __builtin_fmaf(n[4 * i + 3], 16.f, n[4 * i + 2]);
+            h[i] = static_cast<uint32_t>(__builtin_fmaf(hi, 256.f, lo));
+        }
+        w[0] = h[1] << 16 | h[0];
+        w[1] = 0;
+    }
+    return w;
+}
+
+// One wave per token and slice of its rows.  2^lanes_log2 lanes hold a row, 8
+// channels each, so the row's minimum and maximum are a butterfly inside them
+// and a wave takes a group of several heads of K, V or Q at once; what kind of
+// rows a group holds is the same for the whole wave.  kAppendRows groups are
+// in flight, and the rotation's table values stay in registers over them.
+// What bounds it is vector instructions (some 900 a token at 30 heads of 80
+// channels), then the bytes.
 template <typename T, int FMT, typename CT>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 {
-    const int64_t wave = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    const int64_t token = wave / a.slices;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
     if (token >= a.tokens) return;
-    const int lane = threadIdx.x & 63;
-    const int row_lanes = 1 << a.lanes_log2, side = 64 >> a.lanes_log2;
-    const int d0 = (lane & (row_lanes - 1)) * 8;
+    const int slice = blockIdx.y;
+    const int lane = threadIdx.x & 63, d0 = (lane & ((1 << a.lanes_log2) - 1)) * 8, sub = lane >> a.lanes_log2;
     const bool mine = d0 < a.dim;
+    const int d_in = mine ? d0 : 0;
     const int64_t slot = a.slots[token];
     const bool stored = slot >= 0 && slot < a.num_slots;
     const int64_t page = stored ? slot >> a.page_log2 : 0;
     const int off = static_cast<int>(slot & ((1 << a.page_log2) - 1));
+    const int64_t in_page = page * a.page_stride + static_cast<int64_t>(off) * a.token_stride;
+    const T *xk = static_cast<const T *>(a.xk) + token * a.k_ts, *xv = static_cast<const T *>(a.xv) + token * a.v_ts;
+    const T *xq = static_cast<const T *>(a.q) + token * a.q_ts;
+    T *qo = static_cast<T *>(a.qo) + token * a.qo_ts;
     Turn turn;
     turn.on = 0;
-    turn.partner = d0;
     if (mine) load_turn(a, d0, a.table ? a.positions[token] : 0, turn);
+    // half layout, whole runs: the partners come from memory
+    const bool fetch = turn.on && a.half && a.rot % 16 == 0;
+    const int partner = d0 < a.rot / 2 ? d0 + a.rot / 2 : d0 - a.rot / 2;
 
-    const int step = side * a.slices;
-    for (int base = side * static_cast<int>(wave - token * a.slices); base < a.rows; base += step) {
-        const int r = base + (lane >> a.lanes_log2);
-        const bool live = mine && r < a.rows;
-        const int kind = r < a.heads ? 0 : r < 2 * a.heads ? 1 : 2;
-        const int h = kind == 0 ? r : kind == 1 ? r - a.heads : r - 2 * a.heads;
-        float x[8] = {};
-        if (live) {
-            const T *src = kind == 0   ? static_cast<const T *>(a.xk) + token * a.k_ts + h * a.k_hs
-                           : kind == 1 ? static_cast<const T *>(a.xv) + token * a.v_ts + h * a.v_hs
-                                       : static_cast<const T *>(a.q) + token * a.q_ts + h * a.q_hs;
-            load_f32<T, 8>(src + d0, x);
-            if (kind != 1) apply_turn<T>(a, turn, src, d0, x);
-            // q_out may be q: every lane's loads of a row come before its
-            // store, and the lanes of a row are in one wave
-            if (kind == 2) store_f32<T, 8>(static_cast<T *>(a.qo) + token * a.qo_ts + h * a.qo_hs + d0, x);
+    const int kv_groups = (a.heads + (64 >> a.lanes_log2) - 1) >> (6 - a.lanes_log2);
+    for (int g0 = slice; g0 < a.groups; g0 += kAppendRows * a.slices) {
+        int kind[kAppendRows], head[kAppendRows];
+        bool live[kAppendRows];
+        const T *src[kAppendRows];
+        Raw8<T> own[kAppendRows], other[kAppendRows];
+#pragma unroll
+        for (int b = 0; b < kAppendRows; ++b) {
+            const int g = min(g0 + b * a.slices, a.groups - 1);
+            kind[b] = g < kv_groups ? 0 : g < 2 * kv_groups ? 1 : 2;
+            const int limit = kind[b] == 2 ? a.q_heads : a.heads;
+            const int h = ((g - kind[b] * kv_groups) << (6 - a.lanes_log2)) + sub;
+            live[b] = mine && h < limit;
+            head[b] = min(h, limit - 1);
+            src[b] = (kind[b] == 0 ? xk : kind[b] == 1 ? xv : xq) +
+                     head[b] * (kind[b] == 0 ? a.k_hs : kind[b] == 1 ? a.v_hs : a.q_hs);
+            own[b] = load_raw(src[b] + d_in);
+            other[b] = own[b];
+            if (fetch && kind[b] != 1) other[b] = load_raw(src[b] + partner);
         }
-        if constexpr (FMT == PQ_KV_16) {
-            if (live && kind < 2 && stored) {
-                uint8_t *dst = (kind ? a.v : a.k) + page * a.page_stride + h * a.head_stride +
-                               static_cast<int64_t>(off) * a.token_stride + 2 * d0;
+#pragma unroll
+        for (int b = 0; b < kAppendRows; ++b) {
+            if (g0 + b * a.slices >= a.groups) break;
+            float x[8];
+            raw_to_f32<T>(own[b], x);
+            if (kind[b] != 1) apply_turn<T>(a, turn, other[b], src[b], d0, x);
+            if (kind[b] == 2) {
+                // q_out may be q: a row is read and written by lanes of one
+                // wave, which has all it needs of it by now
+                if (live[b]) store_f32<T, 8>(qo + head[b] * a.qo_hs + d0, x);
+                continue;
+            }
+            uint8_t *dst = (kind[b] ? a.v : a.k) + in_page + head[b] * a.head_stride;
+            if constexpr (FMT == PQ_KV_16) {
                 u32x4 w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = pack16<CT>(x[2 * e], x[2 * e + 1]);
-                *reinterpret_cast<u32x4_a8 *>(dst) = w;
-            }
-        } else {
-            constexpr float top = FMT == PQ_KV_8 ? 255.f : 15.f;
-            float mn = __builtin_inff(), mx = -__builtin_inff();
-            if (live) {
+                if (live[b] && stored) *reinterpret_cast<u32x4_a8 *>(dst + 2 * d0) = w;
+            } else {
+                constexpr float top = FMT == PQ_KV_8 ? 255.f : 15.f;
+                float mn = x[0], mx = x[0];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 1; e < 8; ++e) {
                     mn = min_nan(mn, x[e]);
                     mx = max_nan(mx, x[e]);
                 }
-            }
-            for (int o = 1; o < row_lanes; o <<= 1) {
-                mn = min_nan(mn, __shfl_xor(mn, o));
-                mx = max_nan(mx, __shfl_xor(mx, o));
-            }
-            if (live && kind < 2 && stored) {
+                mn = mine ? mn : __builtin_inff();
+                mx = mine ? mx : -__builtin_inff();
+                row_range(a.lanes_log2, mn, mx);
                 const uint32_t sb = pack_bf16x2((mx - mn) * (1.f / top), mn);
                 const float s = fmaxf(bf16_to_f32(sb & 0xFFFFu), kMinKvScale), z = bf16_to_f32(sb >> 16);
                 const float inv = 1.f / s;
-                uint32_t n[8];
+                float n[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // clamped, then rounded to even by the addition of 2^23
-                    const float v = fminf(fmaxf((x[e] - z) * inv, 0.f), top) + 8388608.f;
-                    n[e] = __builtin_bit_cast(uint32_t, v) & 0xFFu;
-                }
-                const int64_t rowoff = page * a.page_stride + h * a.head_stride + static_cast<int64_t>(off) * a.token_stride;
-                uint8_t *dst = (kind ? a.v : a.k) + rowoff;
-                if constexpr (FMT == PQ_KV_8) {
-                    u32x2 w;
-                    w[0] = n[0] | n[1] << 8 | n[2] << 16 | n[3] << 24;
-                    w[1] = n[4] | n[5] << 8 | n[6] << 16 | n[7] << 24;
-                    *reinterpret_cast<u32x2 *>(dst + d0) = w;
-                } else {
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w |= n[e] << (4 * e);
-                    *reinterpret_cast<uint32_t *>(dst + d0 / 2) = w;
-                }
-                if (d0 == 0) {
-                    const uint32_t pair = (__builtin_bit_cast(uint32_t, s) >> 16) | (sb & 0xFFFF0000u);
-                    (kind ? a.vp : a.kp)[((page * a.heads + h) << a.page_log2) + off] = pair;
+                for (int e = 0; e < 8; ++e)
+                    n[e] = __builtin_rintf(__builtin_amdgcn_fmed3f((x[e] - z) * inv, 0.f, top));
+                const u32x2 w = pack_codes<FMT>(n);
+                if (live[b] && stored) {
+                    if constexpr (FMT == PQ_KV_8) *reinterpret_cast<u32x2 *>(dst + d0) = w;
+                    else *reinterpret_cast<uint32_t *>(dst + d0 / 2) = w[0];
+                    if (d0 == 0)
+                        (kind[b] ? a.vp : a.kp)[((page * a.heads + head[b]) << a.page_log2) + off] =
+                            (__builtin_bit_cast(uint32_t, s) >> 16) | (sb & 0xFFFF0000u);
                 }
             }
         }
@@ -220,9 +289,9 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 template <typename T>
 pq_status launch_append(const pq_kv_cache &c, const AppendArgs &a, hipStream_t s)
 {
-    const int64_t blocks = (a.tokens * a.slices + 3) / 4;
+    const int64_t blocks = (a.tokens + 3) / 4;
     if (blocks > INT32_MAX) return PQ_ERR_SHAPE;
-    const dim3 g(static_cast<unsigned>(blocks)), b(256);
+    const dim3 g(static_cast<unsigned>(blocks), static_cast<unsigned>(a.slices)), b(256);
     if (c.format == PQ_KV_8) hipLaunchKernelGGL((k_kv_append<T, PQ_KV_8, bf16_t>), g, b, 0, s, a);
     else if (c.format == PQ_KV_4) hipLaunchKernelGGL((k_kv_append<T, PQ_KV_4, bf16_t>), g, b, 0, s, a);
     else if (c.dtype == PQ_BF16) hipLaunchKernelGGL((k_kv_append<T, PQ_KV_16, bf16_t>), g, b, 0, s, a);
@@ -233,6 +302,7 @@ pq_status launch_append(const pq_kv_cache &c, const AppendArgs &a, hipStream_t s
 // -------------------------------------------------------------------- load
 
 constexpr int kLoadTokens = 16;     // output tokens of a block
+constexpr int kLoadRows = 4;        // rows a thread has in flight
 
 struct LoadArgs {
     const uint8_t *k, *v;
@@ -250,16 +320,13 @@ struct LoadArgs {
 };
 
 // A block takes 16 consecutive output tokens: 16 lanes find their pages (the
-// sequence by a binary search of cu), then the waves walk (head, K or V).  For
-// one head the 16 tokens' rows lie together in a page, so a wave reads whole
-// lines of codes and writes whole rows.
+// sequence by a binary search of cu), then the block walks the tokens' rows.
 template <typename T, int FMT, typename CT>
 __global__ __launch_bounds__(256) void k_kv_load(LoadArgs a)
 {
     __shared__ int s_page[kLoadTokens], s_off[kLoadTokens];
-    const int64_t tile = blockIdx.x / a.slices;
-    const int slice = static_cast<int>(blockIdx.x - tile * a.slices);
-    const int64_t t0 = tile * kLoadTokens;
+    const int slice = blockIdx.y;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kLoadTokens;
     if (threadIdx.x < kLoadTokens) {
         const int64_t i = t0 + threadIdx.x;
         int page = -1, off = 0;
@@ -281,51 +348,69 @@ __global__ __launch_bounds__(256) void k_kv_load(LoadArgs a)
         s_off[threadIdx.x] = off;
     }
     __syncthreads();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row_lanes = 1 << a.lanes_log2, side = 64 >> a.lanes_log2;
-    const int d0 = (lane & (row_lanes - 1)) * 8;
-    if (d0 >= a.dim) return;
-    for (int r = slice * 4 + wave; r < 2 * a.heads; r += 4 * a.slices) {
-        const bool is_v = r >= a.heads;
-        const int h = is_v ? r - a.heads : r;
-        const uint8_t *src = (is_v ? a.v : a.k) + h * a.head_stride;
-        const uint32_t *par = is_v ? a.vp : a.kp;
-        T *out = static_cast<T *>(is_v ? a.vo : a.ko) + (is_v ? a.vo_hs : a.ko_hs) * h + d0;
-        const int64_t ts = is_v ? a.vo_ts : a.ko_ts;
-#pragma unroll 4
-        for (int j = lane >> a.lanes_log2; j < kLoadTokens; j += side) {
-            if (t0 + j >= a.tokens) break;
+    const int row_lanes = 1 << a.lanes_log2;
+    const int d0 = (threadIdx.x & (row_lanes - 1)) * 8;
+    const bool mine = d0 < a.dim;
+    const int side = 256 >> a.lanes_log2;           // rows the block takes at a time
+    const int n = static_cast<int>(a.tokens - t0 < kLoadTokens ? a.tokens - t0 : kLoadTokens) * a.heads;
+    // K and V one after the other, each as one run of (token, head) rows:
+    // side by side in the output, so that the block writes whole stretches.
+    for (int base = slice * side * kLoadRows; base < 2 * n; base += a.slices * side * kLoadRows) {
+        int64_t to[kLoadRows];
+        bool v[kLoadRows], live[kLoadRows];
+        u32x4 w[kLoadRows];
+        uint32_t pair[kLoadRows];
+#pragma unroll
+        for (int k = 0; k < kLoadRows; ++k) {
+            const int r = base + k * side + static_cast<int>(threadIdx.x >> a.lanes_log2);
+            live[k] = mine && r < 2 * n;
+            v[k] = r >= n;
+            const int rr = live[k] ? (v[k] ? r - n : r) : 0;
+            const int j = rr / a.heads, h = rr - j * a.heads;
             const int page = s_page[j], off = s_off[j];
-            float x[8] = {};
-            if (page >= 0) {
-                const uint8_t *p = src + page * a.page_stride + static_cast<int64_t>(off) * a.token_stride;
+            w[k] = u32x4{0, 0, 0, 0};
+            pair[k] = 0;                            // no source: z = s = 0
+            to[k] = (t0 + j) * (v[k] ? a.vo_ts : a.ko_ts) + h * (v[k] ? a.vo_hs : a.ko_hs) + d0;
+            if (live[k] && page >= 0) {
+                const uint8_t *p = (v[k] ? a.v : a.k) + page * a.page_stride + h * a.head_stride +
+                                   static_cast<int64_t>(off) * a.token_stride;
                 if constexpr (FMT == PQ_KV_16) {
-                    const u32x4 w = *reinterpret_cast<const u32x4_a8 *>(p + 2 * d0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) unpack16<CT>(w[e], x[2 * e], x[2 * e + 1]);
+                    w[k] = *reinterpret_cast<const u32x4_a8 *>(p + 2 * d0);
                 } else {
-                    const uint32_t pair = par[((static_cast<int64_t>(page) * a.heads + h) << a.page_log2) + off];
-                    const float s = bf16_to_f32(pair & 0xFFFFu), z = bf16_to_f32(pair >> 16);
+                    pair[k] = (v[k] ? a.vp : a.kp)[((static_cast<int64_t>(page) * a.heads + h) << a.page_log2) + off];
                     if constexpr (FMT == PQ_KV_8) {
-                        const u32x2 w = *reinterpret_cast<const u32x2 *>(p + d0);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = z + s * static_cast<float>(w[e >> 2] >> (8 * (e & 3)) & 0xFFu);
+                        const u32x2 x = *reinterpret_cast<const u32x2 *>(p + d0);
+                        w[k][0] = x[0];
+                        w[k][1] = x[1];
                     } else {
-                        const uint32_t w = *reinterpret_cast<const uint32_t *>(p + d0 / 2);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = z + s * static_cast<float>(w >> (4 * e) & 0xFu);
+                        w[k][0] = *reinterpret_cast<const uint32_t *>(p + d0 / 2);
                     }
                 }
             }
-            store_f32<T, 8>(out + (t0 + j) * ts, x);
+        }
+#pragma unroll
+        for (int k = 0; k < kLoadRows; ++k) {
+            if (!live[k]) continue;
+            float x[8];
+            const float s = bf16_to_f32(pair[k] & 0xFFFFu), z = bf16_to_f32(pair[k] >> 16);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (FMT == PQ_KV_8) x[e] = z + s * static_cast<float>(w[k][e >> 2] >> (8 * (e & 3)) & 0xFFu);
+                if constexpr (FMT == PQ_KV_4) x[e] = z + s * static_cast<float>(w[k][0] >> (4 * e) & 0xFu);
+            }
+            if constexpr (FMT == PQ_KV_16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) unpack16<CT>(w[k][e], x[2 * e], x[2 * e + 1]);
+            }
+            store_f32<T, 8>(static_cast<T *>(v[k] ? a.vo : a.ko) + to[k], x);
         }
     }
 }
 
 template <typename T>
-pq_status launch_load(const pq_kv_cache &c, const LoadArgs &a, unsigned blocks, hipStream_t s)
+pq_status launch_load(const pq_kv_cache &c, const LoadArgs &a, dim3 g, hipStream_t s)
 {
-    const dim3 g(blocks), b(256);
+    const dim3 b(256);
     if (c.format == PQ_KV_8) hipLaunchKernelGGL((k_kv_load<T, PQ_KV_8, bf16_t>), g, b, 0, s, a);
     else if (c.format == PQ_KV_4) hipLaunchKernelGGL((k_kv_load<T, PQ_KV_4, bf16_t>), g, b, 0, s, a);
     else if (c.dtype == PQ_BF16) hipLaunchKernelGGL((k_kv_load<T, PQ_KV_16, bf16_t>), g, b, 0, s, a);
@@ -414,12 +499,11 @@ pq_status pq_kv_append(const pq_kv_cache *cache, int dtype, int64_t tokens, cons
     a.half = layout == PQ_ROPE_HALF;
     a.q_heads = static_cast<int>(q_heads);
     a.lanes_log2 = row_lanes_log2(c.dim);
-    a.rows = 2 * c.heads + a.q_heads;
-    // Few tokens: a token's rows go to several waves, as in the rotation.
+    // Few tokens: a token's row groups go to several waves, as in the rotation.
     const int side = 64 >> a.lanes_log2;
-    const int64_t rounds = (a.rows + side - 1) / side;
+    a.groups = 2 * ((c.heads + side - 1) / side) + (a.q_heads + side - 1) / side;
     int64_t slices = (2048 + tokens - 1) / tokens;
-    if (slices > rounds) slices = rounds;
+    if (slices > a.groups) slices = a.groups;
     a.slices = static_cast<int>(slices);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == PQ_F32) return launch_append<float>(c, a, s);
@@ -473,12 +557,13 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
     a.lanes_log2 = row_lanes_log2(c.dim);
     // Few tokens: the heads of a token tile go to several blocks.
     const int64_t tiles = (tokens + kLoadTokens - 1) / kLoadTokens;
-    const int64_t rounds = (2 * c.heads + 3) / 4;
+    const int64_t per_round = kLoadRows * (256 >> a.lanes_log2);
+    const int64_t rounds = (2 * kLoadTokens * static_cast<int64_t>(c.heads) + per_round - 1) / per_round;
     int64_t slices = (1024 + tiles - 1) / tiles;
     if (slices > rounds) slices = rounds;
     a.slices = static_cast<int>(slices);
-    if (tiles * slices > INT32_MAX) return PQ_ERR_SHAPE;
-    const unsigned blocks = static_cast<unsigned>(tiles * slices);
+    if (tiles > INT32_MAX) return PQ_ERR_SHAPE;
+    const dim3 blocks(static_cast<unsigned>(tiles), static_cast<unsigned>(slices));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == PQ_F32) return launch_load<float>(c, a, blocks, s);
     return dtype == PQ_BF16 ? launch_load<bf16_t>(c, a, blocks, s) : launch_load<f16_t>(c, a, blocks, s);

@@ -53,7 +53,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
 }
 
 // N consecutive elements to fp32 and back; N = 4 or 8 with addresses aligned
-// to min(16, N * sizeof(T)) bytes, or N = 1.
+// to min(16, N * sizeof(T)) bytes, or N = 1.  The cache kernels' vector stores
+// are non-temporal whatever their size: rows need not be whole lines, and a
+// plain store of part of a line waits for the rest of it in L2 (rows of 80
+// channels read back from 4 bits: 63 us against 85; prompts appended 44
+// against 58).
 template <typename T, int N>
 __device__ __forceinline__ void load_f32(const T *p, float (&x)[N])
 {
@@ -77,7 +81,45 @@ __device__ __forceinline__ void load_f32(const T *p, float (&x)[N])
     }
 }
 
-template <typename T, int N>
+// Eight consecutive elements as they lie in memory (a load that does not look
+// at its value yet), and their fp32 values.
+template <typename T>
+struct Raw8 {
+    u32x4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T *p)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const u32x4 *>(p)[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void raw_to_f32(const Raw8<T> &r, float (&x)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const f32x4 a = __builtin_bit_cast(f32x4, r.w[0]), b = __builtin_bit_cast(f32x4, r.w[1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] = a[e];
+            x[4 + e] = b[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack16<T>(r.w[0][e], x[2 * e], x[2 * e + 1]);
+    }
+}
+
+// A vector store, past the caches (NT) or not.
+template <bool NT, typename V>
+__device__ __forceinline__ void store_vec(V *p, V v)
+{
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
+template <typename T, int N, bool NT = true>
 __device__ __forceinline__ void store_f32(T *p, const float (&x)[N])
 {
     if constexpr (N == 1) {
@@ -85,17 +127,17 @@ __device__ __forceinline__ void store_f32(T *p, const float (&x)[N])
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i)
-            reinterpret_cast<f32x4 *>(p)[i] = f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+            store_vec<NT>(reinterpret_cast<f32x4 *>(p) + i, f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]});
     } else if constexpr (N == 8) {
         u32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = pack16<T>(x[2 * e], x[2 * e + 1]);
-        *reinterpret_cast<u32x4 *>(p) = v;
+        store_vec<NT>(reinterpret_cast<u32x4 *>(p), v);
     } else {
         u32x2 v;
 #pragma unroll
         for (int e = 0; e < 2; ++e) v[e] = pack16<T>(x[2 * e], x[2 * e + 1]);
-        *reinterpret_cast<u32x2 *>(p) = v;
+        store_vec<NT>(reinterpret_cast<u32x2 *>(p), v);
     }
 }
 
