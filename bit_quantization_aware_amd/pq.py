@@ -151,8 +151,15 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+# torch's own accessors of the current stream's handle: current_stream() makes
+# a Stream object first, 2.8 us against 0.3, as much as the launch itself.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _current_raw_stream is not None and torch.cuda.is_initialized():
+            return _current_raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -380,29 +387,29 @@ PQ_KV_16, PQ_KV_8, PQ_KV_4 = 0, 1, 2
 _DTYPE = {torch.float32: PQ_F32, torch.bfloat16: PQ_BF16, torch.float16: PQ_F16}
 
 
-def _want(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# Decode steps are short calls, so the checks below are written to cost little:
+# plain conditions, each attribute of a tensor read once.
 
 
 def _dtype(t: torch.Tensor, what: str) -> int:
-    try:
-        return _DTYPE[t.dtype]
-    except KeyError:
-        raise TypeError(f"{what}: {t.dtype} is none of float32, bfloat16, float16") from None
+    d = _DTYPE.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{what}: {t.dtype} is none of float32, bfloat16, float16")
+    return d
 
 
 def _rows(t: torch.Tensor, what: str):
     """(token stride, head stride) in elements of t [tokens, heads, dim]."""
-    _want(t.dim() == 3, f"{what}: [tokens, heads, dim] wanted")
-    a, b, c = t.stride()
-    _want(c == 1 or t.shape[2] == 1, f"{what}: the last dimension has to be contiguous")
-    return a, b
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and t.shape[2] != 1):
+        raise ValueError(f"{what}: [tokens, heads, dim] with a contiguous last dimension wanted")
+    return st[0], st[1]
 
 
 def _array(t: torch.Tensor, dtype: torch.dtype, n: int, what: str) -> int:
     """The address of a contiguous index array of n elements."""
-    _want(t.dtype == dtype and t.numel() == n and t.is_contiguous(), f"{what}: {n} contiguous {dtype} wanted")
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous {dtype} wanted")
     return t.data_ptr()
 
 
@@ -426,22 +433,30 @@ def rope_scaling(kind, factor, trained=0.0, beta_fast=None, beta_slow=1.0) -> pq
 
 
 def _table_shape(table: torch.Tensor):
-    _want(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2 and table.is_contiguous(),
-          "table: contiguous float32 [max_pos, rot / 2, 2] wanted")
-    return table.shape[0], 2 * table.shape[1]
+    n = table.shape
+    if len(n) != 3 or n[2] != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table: contiguous float32 [max_pos, rot / 2, 2] wanted")
+    return n[0], 2 * n[1]
 
 
 def pq_rope(x, positions, table, y=None, layout=PQ_ROPE_HALF, inverse=False, stream=None) -> None:
     """Rotate x [tokens, heads, dim] into y (None: in place); inverse=True is the gradient's rotation."""
-    y = x if y is None else y
-    _want(y.shape == x.shape and y.dtype == x.dtype, "y: the shape and type of x wanted")
+    n, heads, dim = shape = x.shape
     xt, xh = _rows(x, "x")
-    yt, yh = _rows(y, "y")
-    n, heads, dim = x.shape
+    xp = x.data_ptr()
+    if y is None:
+        yp, yt, yh = xp, xt, xh
+    else:
+        if y.shape != shape or y.dtype != x.dtype:
+            raise ValueError("y: the shape and type of x wanted")
+        yp = y.data_ptr()
+        yt, yh = _rows(y, "y")
     max_pos, rot = _table_shape(table)
-    _check(lib.pq_rope(_dtype(x, "x"), n, heads, dim, rot, layout, 1 if inverse else 0, x.data_ptr(), xt, xh,
-                       _array(positions, torch.int32, n, "positions"), table.data_ptr(), max_pos, y.data_ptr(), yt, yh,
-                       _stream(stream)), "pq_rope")
+    rc = lib.pq_rope(_dtype(x, "x"), n, heads, dim, rot, layout, 1 if inverse else 0, xp, xt, xh,
+                     _array(positions, torch.int32, n, "positions"), table.data_ptr(), max_pos, yp, yt, yh,
+                     _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_rope")
 
 
 def pq_kv_row_bytes(fmt: int, dim: int) -> int:
@@ -458,20 +473,25 @@ class KVCache:
     [pages, heads, page_size, 2]."""
 
     def __init__(self, fmt, page_size, k, v, k_param=None, v_param=None):
-        _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype,
-              "k, v: [pages, heads, page_size, row] of one type, shape and strides wanted")
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k, v: [pages, heads, page_size, row] of one type, shape and strides wanted")
         pages, heads, tokens, row = k.shape
-        _want(tokens == page_size and k.stride(3) == 1, "k, v: page_size tokens of contiguous rows wanted")
-        _want(fmt in (PQ_KV_16, PQ_KV_8, PQ_KV_4), "fmt: PQ_KV_16, PQ_KV_8 or PQ_KV_4 wanted")
+        if tokens != page_size or k.stride(3) != 1:
+            raise ValueError("k, v: page_size tokens of contiguous rows wanted")
         if fmt == PQ_KV_16:
-            _want(k.dtype in (torch.bfloat16, torch.float16), "k, v: bfloat16 or float16 wanted")
+            if k.dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError("k, v: bfloat16 or float16 wanted")
             dim, dtype = row, _DTYPE[k.dtype]
-        else:
-            _want(k.dtype == torch.uint8, "k, v: uint8 wanted")
+        elif fmt in (PQ_KV_8, PQ_KV_4):
+            if k.dtype != torch.uint8:
+                raise ValueError("k, v: uint8 wanted")
             dim, dtype = row * (1 if fmt == PQ_KV_8 else 2), 0
             for p in (k_param, v_param):
-                _want(p is not None and p.dtype == torch.bfloat16 and tuple(p.shape) == (pages, heads, tokens, 2) and
-                      p.is_contiguous(), "k_param, v_param: contiguous bfloat16 [pages, heads, page_size, 2] wanted")
+                if p is None or p.dtype != torch.bfloat16 or tuple(p.shape) != (pages, heads, tokens, 2) or \
+                        not p.is_contiguous():
+                    raise ValueError("k_param, v_param: contiguous bfloat16 [pages, heads, page_size, 2] wanted")
+        else:
+            raise ValueError("fmt: PQ_KV_16, PQ_KV_8 or PQ_KV_4 wanted")
         self.tensors = (k, v, k_param, v_param)          # kept alive with the addresses
         self.format, self.page_size, self.heads, self.dim, self.num_pages = fmt, page_size, heads, dim, pages
         size = k.element_size()
@@ -496,46 +516,61 @@ def pq_kv_append(cache: KVCache, k, v, slots, positions=None, table=None, layout
                  stream=None) -> None:
     """Write k, v [tokens, heads, dim] into the cache at slots; with a table k is rotated on the way, and q
     [tokens, q_heads, dim] is rotated into q_out (None: in place) in the same launch."""
-    n = k.shape[0]
+    n, heads, dim = shape = k.shape
     kt, kh = _rows(k, "k")
     vt, vh = _rows(v, "v")
-    _want(k.shape == v.shape and k.dtype == v.dtype and tuple(k.shape[1:]) == (cache.heads, cache.dim),
-          "k, v: [tokens, heads, dim] of the cache and one type wanted")
-    max_pos, rot, pp, tp = 0, 0, None, None
+    kind = k.dtype
+    if v.shape != shape or v.dtype != kind or heads != cache.heads or dim != cache.dim:
+        raise ValueError("k, v: [tokens, heads, dim] of the cache and one type wanted")
+    max_pos = rot = qh = qt = qs = qot = qos = 0
+    pp = tp = qp = qop = None
     if table is not None:
         max_pos, rot = _table_shape(table)
         tp = table.data_ptr()
-        pp = None if positions is None else _array(positions, torch.int32, n, "positions")
-    qh, qp, qop, qs, qos = 0, None, None, (0, 0), (0, 0)
+        if positions is not None:
+            pp = _array(positions, torch.int32, n, "positions")
     if q is not None:
-        q_out = q if q_out is None else q_out
-        qs, qos = _rows(q, "q"), _rows(q_out, "q_out")
-        _want(q_out.shape == q.shape and q.shape[0] == n and q.shape[2] == cache.dim and q.dtype == k.dtype and
-              q_out.dtype == k.dtype, "q, q_out: [tokens, q_heads, dim] of k's type wanted")
-        qh, qp, qop = q.shape[1], q.data_ptr(), q_out.data_ptr()
-    _check(lib.pq_kv_append(cache.ptr, _dtype(k, "k"), n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                            _array(slots, torch.int64, n, "slots"), pp, tp, max_pos, rot, layout, qp, qh, qs[0], qs[1],
-                            qop, qos[0], qos[1], _stream(stream)), "pq_kv_append")
+        qn, qh, qd = qshape = q.shape
+        if qn != n or qd != dim or q.dtype != kind:
+            raise ValueError("q: [tokens, q_heads, dim] of k's type wanted")
+        qt, qs = _rows(q, "q")
+        qp = q.data_ptr()
+        if q_out is None:
+            qop, qot, qos = qp, qt, qs
+        else:
+            if q_out.shape != qshape or q_out.dtype != kind:
+                raise ValueError("q_out: the shape and type of q wanted")
+            qot, qos = _rows(q_out, "q_out")
+            qop = q_out.data_ptr()
+    rc = lib.pq_kv_append(cache.ptr, _dtype(k, "k"), n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                          _array(slots, torch.int64, n, "slots"), pp, tp, max_pos, rot, layout, qp, qh, qt, qs,
+                          qop, qot, qos, _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_kv_append")
 
 
 def _block_table(block_table, batch: int):
-    _want(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == batch and
-          (block_table.stride(1) == 1 or block_table.shape[1] <= 1), "block_table: int32 [batch, pages] wanted")
-    return block_table.data_ptr(), block_table.stride(0), block_table.shape[1]
+    n, st = block_table.shape, block_table.stride()
+    if len(n) != 2 or n[0] != batch or (st[1] != 1 and n[1] > 1) or block_table.dtype != torch.int32:
+        raise ValueError("block_table: int32 [batch, pages] wanted")
+    return block_table.data_ptr(), st[0], n[1]
 
 
 def pq_kv_load(cache: KVCache, block_table, starts, cu, k_out, v_out, stream=None) -> None:
     """Read tokens starts[b] .. of each sequence into rows cu[b] .. cu[b + 1] of k_out and v_out."""
     batch = cu.numel() - 1
     bp, bs, bn = _block_table(block_table, batch)
-    _want(k_out.shape == v_out.shape and k_out.dtype == v_out.dtype and
-          tuple(k_out.shape[1:]) == (cache.heads, cache.dim), "k_out, v_out: [tokens, heads, dim] of one type wanted")
+    n, heads, dim = shape = k_out.shape
+    if v_out.shape != shape or v_out.dtype != k_out.dtype or heads != cache.heads or dim != cache.dim:
+        raise ValueError("k_out, v_out: [tokens, heads, dim] of one type wanted")
     kt, kh = _rows(k_out, "k_out")
     vt, vh = _rows(v_out, "v_out")
-    _check(lib.pq_kv_load(cache.ptr, _dtype(k_out, "k_out"), batch, k_out.shape[0], bp, bs, bn,
-                          None if starts is None else _array(starts, torch.int32, batch, "starts"),
-                          _array(cu, torch.int32, batch + 1, "cu"), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh,
-                          _stream(stream)), "pq_kv_load")
+    rc = lib.pq_kv_load(cache.ptr, _dtype(k_out, "k_out"), batch, n, bp, bs, bn,
+                        None if starts is None else _array(starts, torch.int32, batch, "starts"),
+                        _array(cu, torch.int32, batch + 1, "cu"), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh,
+                        _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_kv_load")
 
 
 def pq_attn_decode_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> int:
@@ -554,17 +589,20 @@ def pq_attn_decode(cache: KVCache, q, block_table, lens, out, lse=None, scale=No
                    workspace=None, stream=None) -> None:
     """Attention of one new token per sequence, q [batch, q_heads, dim], over the cache; scale defaults to
     1 / sqrt(dim).  Without a workspace one is allocated for the call."""
-    batch, q_heads, dim = q.shape
-    _want(dim == cache.dim and out.shape == q.shape and out.dtype == q.dtype, "q, out: [batch, q_heads, dim] wanted")
-    qs, os_ = _rows(q, "q"), _rows(out, "out")
+    batch, q_heads, dim = shape = q.shape
+    if dim != cache.dim or out.shape != shape or out.dtype != q.dtype:
+        raise ValueError("q, out: [batch, q_heads, dim] of the cache and one type wanted")
+    qt, qh = _rows(q, "q")
+    ot, oh = _rows(out, "out")
     bp, bs, bn = _block_table(block_table, batch)
     if workspace is None:
         workspace = attn_workspace(cache, batch, q_heads, q.device)
         if stream is not None:
             workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    _check(lib.pq_attn_decode(cache.ptr, _dtype(q, "q"), batch, q_heads, q.data_ptr(), qs[0], qs[1], bp, bs, bn,
-                              _array(lens, torch.int32, batch, "lens"), dim ** -0.5 if scale is None else float(scale),
-                              window, max_len, out.data_ptr(), os_[0], os_[1],
-                              None if lse is None else _array(lse, torch.float32, batch * q_heads, "lse"),
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
-           "pq_attn_decode")
+    rc = lib.pq_attn_decode(cache.ptr, _dtype(q, "q"), batch, q_heads, q.data_ptr(), qt, qh, bp, bs, bn,
+                            _array(lens, torch.int32, batch, "lens"), dim ** -0.5 if scale is None else scale, window,
+                            max_len, out.data_ptr(), ot, oh,
+                            None if lse is None else _array(lse, torch.float32, batch * q_heads, "lse"),
+                            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_attn_decode")
