@@ -174,15 +174,31 @@ __device__ __forceinline__ float column_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// A wave-uniform address in scalar registers, its sum closed to the compiler:
-// it would else add the lane's offset to the base first and spend a 64-bit
-// vector addition per load.
-__device__ __forceinline__ const PQ_GLOBAL uint8_t *scalar_address(const uint8_t *p)
-{
-    uint64_t u = reinterpret_cast<uint64_t>(p);
-    asm("" : "+s"(u));
-    return reinterpret_cast<const PQ_GLOBAL uint8_t *>(u);
-}
+// Loads at a 32-bit offset of the lane from a wave-uniform address: buffer
+// loads, whose resource is made from the address in scalar registers.  From a
+// pointer the compiler adds the two in every lane, 64 bits wide, 24 times a
+// step (the offsets' extensions leave the loop, and with them the proof that
+// they are 32-bit ones).  `bytes`: what may be read there.
+struct Resource {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ Resource(const uint8_t *p, int bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, bytes, 0x00027000)) {}     // raw, 32-bit data
+    template <bool NT>
+    __device__ __forceinline__ u32x4 load16(uint32_t at) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, NT ? 2 : 0);     // 2: non-temporal
+    }
+    template <bool NT>
+    __device__ __forceinline__ u32x2 load8(uint32_t at) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, NT ? 2 : 0);
+    }
+    __device__ __forceinline__ uint32_t load4(uint32_t at) const { return __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0); }
+    __device__ __forceinline__ uint32_t load2(uint32_t at) const
+    {
+        return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+    }
+};
 
 template <bool F16>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
@@ -191,20 +207,6 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-// 16 and 8 bytes at a multiple of 8.
-template <bool NT>
-__device__ __forceinline__ u32x4 load16(const PQ_GLOBAL uint8_t *p)
-{
-    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(p));
-    else return *reinterpret_cast<const PQ_GLOBAL u32x4_a8 *>(p);
-}
-template <bool NT>
-__device__ __forceinline__ u32x2 load8(const PQ_GLOBAL uint8_t *p)
-{
-    if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const PQ_GLOBAL u32x2 *>(p));
-    else return *reinterpret_cast<const PQ_GLOBAL u32x2 *>(p);
 }
 
 // QT: type of q and out (and of a 16-bit cache).  FMT: cache format.  DP: dim
@@ -318,10 +320,10 @@ struct Attn {
         for (int e = 0; e < E; ++e) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Byte offsets of the lane's loads from a 16-token tile's first row; with
-    // the tile's wave-uniform address they are the hardware's base + 32-bit
-    // offset form.  Channels past dim: any, q is 0 there.
+    // Byte offsets of the lane's loads from a 16-token tile's first row, and
+    // the tile's bytes.  Channels past dim: any, q is 0 there.
     uint32_t k_off, k_last, v_off, v_step, v_second;
+    int tile_bytes;
 
     __device__ __forceinline__ void set_offsets(const AttnArgs &a)
     {
@@ -334,20 +336,21 @@ struct Attn {
         v_second = 2 * (min(128u + column() * kRun, static_cast<uint32_t>(a.dim - kRun)) - d);
         v_off = 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
         v_step = a.token_stride;
+        tile_bytes = 15 * a.token_stride + row_bytes;
     }
 
     __device__ __forceinline__ void load_k(int r, int tile, const uint8_t *tile_row)
     {
-        const PQ_GLOBAL uint8_t *row = scalar_address(tile_row);
+        const Resource rows(tile_row, tile_bytes);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
             const uint32_t at = min(k_off + c * (KW * 16), k_last);
             if constexpr (KW == 2) {
-                const u32x2 w = *reinterpret_cast<const PQ_GLOBAL u32x2 *>(row + at);
+                const u32x2 w = rows.template load8<NT>(at);
                 k[r][tile][c][0] = w[0];
                 k[r][tile][c][1] = w[1];
             } else {
-                const u32x4 w = load16<NT>(row + at);
+                const u32x4 w = rows.template load16<NT>(at);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) k[r][tile][c][e] = w[e];
             }
@@ -356,24 +359,24 @@ struct Attn {
 
     __device__ __forceinline__ void load_v(int r, int tile, const uint8_t *tile_row)
     {
-        const PQ_GLOBAL uint8_t *row = scalar_address(tile_row);
+        const Resource rows(tile_row, tile_bytes);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const PQ_GLOBAL uint8_t *t = row + (v_off + j * v_step);
+            const uint32_t t = v_off + j * v_step;
             uint32_t(&w)[VW] = v[r][tile][j];
             if constexpr (FMT == PQ_KV_4 && E == 4) {
-                w[0] = *reinterpret_cast<const PQ_GLOBAL uint16_t *>(t);
+                w[0] = rows.load2(t);
             } else if constexpr (VW == 1) {
-                w[0] = *reinterpret_cast<const PQ_GLOBAL uint32_t *>(t);
+                w[0] = rows.load4(t);
             } else if constexpr (VW == 2) {
-                const u32x2 x = load8<NT>(t);
+                const u32x2 x = rows.template load8<NT>(t);
                 w[0] = x[0];
                 w[1] = x[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < VW / 4; ++i) {
                     // a second run (16-bit rows of over 128 channels) lies 128 channels on
-                    const u32x4 x = load16<NT>(i ? t + v_second : t);
+                    const u32x4 x = rows.template load16<NT>(i ? t + v_second : t);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
                 }
