@@ -239,6 +239,7 @@ struct Attn {
     u32x4 q[KS];
     f32x4 o[E];
     float m, l, zsum;
+    float ref, limit;               // m - kShift; the y that moves m
     float c1, c2;                   // x = s_k (acc c1) + (z_k + s_k c) c2   (16-bit rows: x = acc c1)
     f32x4 acc0;                     // start of the first product
     uint32_t k[R][2][KC][KW], v[R][2][4][VW];   // two 16-token tiles per block; V: tokens 4 kb + j
@@ -313,7 +314,8 @@ struct Attn {
 
     __device__ __forceinline__ void clear()
     {
-        m = -__builtin_inff();
+        m = limit = -__builtin_inff();
+        ref = -kShift;
         l = 0.f;
         zsum = 0.f;
 #pragma unroll
@@ -447,24 +449,26 @@ struct Attn {
     }
 
     // Scores to weights, as operands.  `seen`: bit i for token 4 kb + i of the
-    // own block's first tile, bit 4 + i of its second.
+    // own block's first tile, bit 4 + i of its second.  Everything is relative
+    // to `ref` = m - kShift, which goes in with the constant of a token's row.
     __device__ __forceinline__ void softmax(float (&x)[8], unsigned seen, bool masked, u32x4 &hi, u32x4 &lo)
     {
-        float y[8];                 // x + log2 s_v: the exponent of the weight of the codes
+        float y[8];                 // x + log2 s_v (+ kBias): the exponent of the weight of the codes
         float sv[8], zv[8];
+        constexpr float kBias = kRaw ? 0.f : 127.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if constexpr (kRaw) {
-                y[i] = x[i] = x[i] * c1;
+                y[i] = x[i] = __builtin_fmaf(x[i], c1, -ref);
             } else {
                 constexpr float mid = FMT == PQ_KV_8 ? 128.f : 8.f;
                 const uint32_t kw = kpar[i >> 2][i & 3], vw = vpar[i >> 2][i & 3];
                 const float sk = __builtin_bit_cast(float, kw << 16), zk = __builtin_bit_cast(float, kw & 0xFFFF0000u);
                 sv[i] = __builtin_bit_cast(float, vw << 16);
                 zv[i] = __builtin_bit_cast(float, vw & 0xFFFF0000u);
-                x[i] = __builtin_fmaf(sk, x[i] * c1, __builtin_fmaf(sk, mid, zk) * c2);
+                x[i] = __builtin_fmaf(sk, x[i] * c1, __builtin_fmaf(__builtin_fmaf(sk, mid, zk), c2, -ref));
                 // the bits of a positive float are 2^23 (127 + log2) to within 0.09 octaves
-                y[i] = __builtin_fmaf(static_cast<float>(vw << 16), 0x1p-23f, x[i]) - 127.f;
+                y[i] = __builtin_fmaf(static_cast<float>(vw << 16), 0x1p-23f, x[i]);
             }
         }
         if (masked) {
@@ -485,20 +489,24 @@ struct Attn {
             }
         }
         const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-        if (__ballot(top > m + kSlack)) {           // also the first step: m is -inf
-            const float mn = fmaxf(m, column_max(top));
+        if (__ballot(top > limit)) {                // also the first step: limit is -inf
+            const float mn = fmaxf(m, column_max(top) + (ref - kBias));
             const float f = m == mn ? 1.f : exp2_fast(m - mn);
+            const float next = mn == -__builtin_inff() ? ref : mn - kShift, by = ref - next;
             m = mn;
+            ref = next;
+            limit = mn == -__builtin_inff() ? -__builtin_inff() : kShift + kSlack + kBias;
             l *= f;
             zsum *= f;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += by;
         }
-        const float ref = (m == -__builtin_inff() ? 0.f : m) - kShift;
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float p = exp2_fast(x[i] - ref);
+            const float p = exp2_fast(x[i]);
             l += p;
             if constexpr (kRaw) {
                 w[i] = p;
@@ -511,7 +519,9 @@ struct Attn {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hi[i] = pack16<OT>(w[2 * i], w[2 * i + 1]);
+            // f16: the first is cut off, in one operation for both; the second has what is left
+            if constexpr (kF16) hi[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(w[2 * i], w[2 * i + 1]));
+            else hi[i] = pack16<OT>(w[2 * i], w[2 * i + 1]);
             float h0, h1;
             unpack16<OT>(hi[i], h0, h1);
             lo[i] = pack16<OT>(w[2 * i] - h0, w[2 * i + 1] - h1);
