@@ -63,6 +63,7 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxBatch = 1024;     // sequences of one launch (their step counts sit in LDS)
@@ -428,7 +429,8 @@ struct Attn {
                 f[i] = __builtin_amdgcn_perm(~w1[e >> 2], w0[e >> 2], 0x0c000c00u | b | (b + 4) << 16);
             } else {
                 const uint32_t b = (e >> 1) & 3, up = e & 1 ? 0 : 4, nibble = 0xF0F0F0F0u;
-                f[i] = __builtin_amdgcn_perm(~(w1[e >> 3] << up) & nibble, w0[e >> 3] << up & nibble, 0x0c000c00u | b | (b + 4) << 16);
+                const uint32_t n1 = __builtin_amdgcn_bitop3_b32(w1[e >> 3] << up, nibble, 0, 0x0C);    // ~a & b
+                f[i] = __builtin_amdgcn_perm(n1, w0[e >> 3] << up & nibble, 0x0c000c00u | b | (b + 4) << 16);
             }
         }
         return f;
@@ -524,7 +526,14 @@ struct Attn {
             else hi[i] = pack16<OT>(w[2 * i], w[2 * i + 1]);
             float h0, h1;
             unpack16<OT>(hi[i], h0, h1);
-            lo[i] = pack16<OT>(w[2 * i] - h0, w[2 * i + 1] - h1);
+            if constexpr (kF16) {
+                // written as multiply-adds: one operation takes the f16, subtracts and rounds to f16
+                const f16x2_t r = {static_cast<_Float16>(__builtin_fmaf(-h0, 1.f, w[2 * i])),
+                                   static_cast<_Float16>(__builtin_fmaf(-h1, 1.f, w[2 * i + 1]))};
+                lo[i] = __builtin_bit_cast(uint32_t, r);
+            } else {
+                lo[i] = pack16<OT>(w[2 * i] - h0, w[2 * i + 1] - h1);
+            }
         }
     }
 
@@ -669,23 +678,25 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
 #pragma unroll
         for (int t = 0; t < kIds; ++t) st.load_v(t >> 1, t & 1, a.v + tile_at[t]);
     };
+    const uint64_t v_from_k = reinterpret_cast<uint64_t>(a.vp) - reinterpret_cast<uint64_t>(a.kp);
     auto load_pairs = [&](int kvh, const Step &f) {
         if constexpr (!A::kRaw) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                int64_t at[R];
+                uint64_t at[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int id = f.id[2 * r + t];
-                    at[r] = ((static_cast<int64_t>(valid(id) ? id : 0) * a.heads + kvh) << a.page_log2) +
-                            ((f.t + (2 * r + t) * 16) & in_page);
+                    at[r] = reinterpret_cast<uint64_t>(
+                        a.kp + ((static_cast<int64_t>(valid(id) ? id : 0) * a.heads + kvh) << a.page_log2) +
+                        ((f.t + (2 * r + t) * 16) & in_page));
                 }
-                int64_t p = at[0];
+                uint64_t p = at[0];
 #pragma unroll
                 for (int r = 1; r < R; ++r) p = A::copy() == r ? at[r] : p;
-                p += 4 * kb;
-                st.kpar[t] = *reinterpret_cast<const u32x4 *>(a.kp + p);
-                st.vpar[t] = *reinterpret_cast<const u32x4 *>(a.vp + p);
+                p += 16 * kb;
+                st.kpar[t] = *reinterpret_cast<const PQ_GLOBAL u32x4 *>(p);
+                st.vpar[t] = *reinterpret_cast<const PQ_GLOBAL u32x4 *>(p + v_from_k);
             }
         }
     };
