@@ -20,6 +20,16 @@
 namespace pq {
 namespace {
 
+// The lanes of a row, 8 channels each (an even number: dim is a multiple of
+// 16), rows side by side without a gap.
+struct RowLanes {
+    int n, inverse;                 // 2^16 / n, rounded up: lane / n = lane * inverse >> 16 for lanes below 256
+    int side;                       // rows of a wave
+    RowLanes() = default;
+    explicit RowLanes(int dim) : n(dim / 8), inverse((65536 + n - 1) / n), side(64 / n) {}
+    __device__ __forceinline__ int row(int lane) const { return lane * inverse >> 16; }
+};
+
 // ------------------------------------------------------------------ append
 
 // Row groups a wave has in flight: one, and six waves per SIMD (14 Ki tokens of
@@ -39,8 +49,8 @@ struct AppendArgs {
     const float *table;             // NULL: no rotation
     int64_t tokens;
     int max_pos, rot, half, q_heads;
-    int lanes_log2;                 // log2 of the lanes of a row (8 channels each)
-    int groups, slices;             // row groups of a token (K, V, Q); waves per token
+    RowLanes lanes;
+    int kv_groups, groups, slices;  // row groups of a token: of K and of V each, of K, V and Q; waves per token
 };
 
 // The rotation of one lane's 8 channels d0 .. d0 + 7: y = x c + partner s per
@@ -129,31 +139,60 @@ __device__ __forceinline__ void apply_turn(const AppendArgs &a, const Turn &t, c
 __device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
 __device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
-// Minimum and maximum over the 2^l lanes of a row: neighbours, pairs, quads and
-// eights exchange by DPP (mirrors serve, since the lanes of a half agree).
+// Minimum and maximum over the n lanes of a row.  Powers of two: neighbours,
+// pairs, quads and eights exchange by DPP (mirrors serve, since the lanes of a
+// half agree).  Others: the row's n / 2 pairs as a ring, each looking ahead
+// over what it has covered so far, and no further than around; `ring` holds
+// the steps' source lanes, four bytes a lane.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
 }
-__device__ __forceinline__ void row_range(int l, float &mn, float &mx)
+__device__ __forceinline__ float from_lane(int at, float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(at, __builtin_bit_cast(int, x)));
+}
+constexpr int kRingSteps = 4;       // up to 16 pairs
+__device__ __forceinline__ void set_ring(int n, int lane, int in_row, int (&ring)[kRingSteps])
+{
+    int covered = 1;
+#pragma unroll
+    for (int i = 0; i < kRingSteps; ++i) {
+        const int ahead = min(covered, n / 2 - covered), to = in_row + 2 * ahead;
+        ring[i] = 4 * (lane - in_row + (to < n ? to : to - n));
+        covered += ahead;
+    }
+}
+__device__ __forceinline__ void row_range(int n, const int (&ring)[kRingSteps], float &mn, float &mx)
 {
     constexpr int kPairs = 0xB1, kQuads = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;   // quad_perm 1 0 3 2; 2 3 0 1
     mn = min_nan(mn, dpp<kPairs>(mn));
     mx = max_nan(mx, dpp<kPairs>(mx));
-    if (l >= 2) {
+    if (n & (n - 1)) {
+        int covered = 1;
+#pragma unroll
+        for (int i = 0; i < kRingSteps; ++i) {
+            if (covered >= n / 2) break;
+            mn = min_nan(mn, from_lane(ring[i], mn));
+            mx = max_nan(mx, from_lane(ring[i], mx));
+            covered *= 2;
+        }
+        return;
+    }
+    if (n >= 4) {
         mn = min_nan(mn, dpp<kQuads>(mn));
         mx = max_nan(mx, dpp<kQuads>(mx));
     }
-    if (l >= 3) {
+    if (n >= 8) {
         mn = min_nan(mn, dpp<kHalfMirror>(mn));
         mx = max_nan(mx, dpp<kHalfMirror>(mx));
     }
-    if (l >= 4) {
+    if (n >= 16) {
         mn = min_nan(mn, dpp<kMirror>(mn));
         mx = max_nan(mx, dpp<kMirror>(mx));
     }
-    if (l >= 5) {
+    if (n >= 32) {
         mn = min_nan(mn, __shfl_xor(mn, 16));
         mx = max_nan(mx, __shfl_xor(mx, 16));
     }
@@ -185,10 +224,11 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&n)[8])
     return w;
 }
 
-// One wave per token and slice of its rows.  2^lanes_log2 lanes hold a row, 8
-// channels each, so the row's minimum and maximum are a butterfly inside them
-// and a wave takes a group of several heads of K, V or Q at once; what kind of
-// rows a group holds is the same for the whole wave.  kAppendRows groups are
+// One wave per token and slice of its rows.  dim / 8 lanes hold a row, 8
+// channels each, and a wave takes a group of as many heads of K, V or Q as fit
+// at once (rows of 80 channels in 16 lanes each, with a butterfly in them,
+// waste six: 14 Ki tokens of 30 heads 38 us against 30); what kind of rows a group holds is the same
+// for the whole wave.  kAppendRows groups are
 // in flight, and the rotation's table values stay in registers over them.
 // What bounds it is vector instructions (some 900 a token at 30 heads of 80
 // channels), then the bytes.
@@ -199,9 +239,10 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     const int64_t token = static_cast<int64_t>(blockIdx.x) * 4 + wave;
     if (token >= a.tokens) return;
     const int slice = blockIdx.y;
-    const int lane = threadIdx.x & 63, d0 = (lane & ((1 << a.lanes_log2) - 1)) * 8, sub = lane >> a.lanes_log2;
-    const bool mine = d0 < a.dim;
-    const int d_in = mine ? d0 : 0;
+    const int lane = threadIdx.x & 63, sub = a.lanes.row(lane), in_row = lane - sub * a.lanes.n, d0 = 8 * in_row;
+    const bool mine = sub < a.lanes.side;
+    int ring[kRingSteps];
+    if constexpr (FMT != PQ_KV_16) set_ring(a.lanes.n, lane, in_row, ring);
     const int64_t slot = a.slots[token];
     const bool stored = slot >= 0 && slot < a.num_slots;
     const int64_t page = stored ? slot >> a.page_log2 : 0;
@@ -217,7 +258,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     const bool fetch = turn.on && a.half && a.rot % 16 == 0;
     const int partner = d0 < a.rot / 2 ? d0 + a.rot / 2 : d0 - a.rot / 2;
 
-    const int kv_groups = (a.heads + (64 >> a.lanes_log2) - 1) >> (6 - a.lanes_log2);
+    const int kv_groups = a.kv_groups;
     for (int g0 = slice; g0 < a.groups; g0 += kAppendRows * a.slices) {
         int kind[kAppendRows], head[kAppendRows];
         bool live[kAppendRows];
@@ -228,12 +269,12 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
             const int g = min(g0 + b * a.slices, a.groups - 1);
             kind[b] = g < kv_groups ? 0 : g < 2 * kv_groups ? 1 : 2;
             const int limit = kind[b] == 2 ? a.q_heads : a.heads;
-            const int h = ((g - kind[b] * kv_groups) << (6 - a.lanes_log2)) + sub;
+            const int h = (g - kind[b] * kv_groups) * a.lanes.side + sub;
             live[b] = mine && h < limit;
             head[b] = min(h, limit - 1);
             src[b] = (kind[b] == 0 ? xk : kind[b] == 1 ? xv : xq) +
                      head[b] * (kind[b] == 0 ? a.k_hs : kind[b] == 1 ? a.v_hs : a.q_hs);
-            own[b] = load_raw(src[b] + d_in);
+            own[b] = load_raw(src[b] + d0);
             other[b] = own[b];
             if (fetch && kind[b] != 1) other[b] = load_raw(src[b] + partner);
         }
@@ -263,9 +304,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
                     mn = min_nan(mn, x[e]);
                     mx = max_nan(mx, x[e]);
                 }
-                mn = mine ? mn : __builtin_inff();
-                mx = mine ? mx : -__builtin_inff();
-                row_range(a.lanes_log2, mn, mx);
+                row_range(a.lanes.n, ring, mn, mx);
                 const uint32_t sb = pack_bf16x2((mx - mn) * (1.f / top), mn);
                 const float s = fmaxf(bf16_to_f32(sb & 0xFFFFu), kMinKvScale), z = bf16_to_f32(sb >> 16);
                 const float inv = 1.f / s;
@@ -316,7 +355,8 @@ struct LoadArgs {
     int64_t tokens;
     void *ko, *vo;
     int64_t ko_ts, ko_hs, vo_ts, vo_hs;
-    int lanes_log2, slices;         // lanes of a row (8 channels each); blocks per token tile
+    RowLanes lanes;
+    int slices;                     // blocks per token tile
 };
 
 // A block takes 16 consecutive output tokens: 16 lanes find their pages (the
@@ -348,10 +388,9 @@ __global__ __launch_bounds__(256) void k_kv_load(LoadArgs a)
         s_off[threadIdx.x] = off;
     }
     __syncthreads();
-    const int row_lanes = 1 << a.lanes_log2;
-    const int d0 = (threadIdx.x & (row_lanes - 1)) * 8;
-    const bool mine = d0 < a.dim;
-    const int side = 256 >> a.lanes_log2;           // rows the block takes at a time
+    const int sub = a.lanes.row(threadIdx.x), d0 = 8 * (static_cast<int>(threadIdx.x) - sub * a.lanes.n);
+    const int side = 256 / a.lanes.n;               // rows the block takes at a time
+    const bool mine = sub < side;
     const int n = static_cast<int>(a.tokens - t0 < kLoadTokens ? a.tokens - t0 : kLoadTokens) * a.heads;
     // K and V one after the other, each as one run of (token, head) rows:
     // side by side in the output, so that the block writes whole stretches.
@@ -362,7 +401,7 @@ __global__ __launch_bounds__(256) void k_kv_load(LoadArgs a)
         uint32_t pair[kLoadRows];
 #pragma unroll
         for (int k = 0; k < kLoadRows; ++k) {
-            const int r = base + k * side + static_cast<int>(threadIdx.x >> a.lanes_log2);
+            const int r = base + k * side + sub;
             live[k] = mine && r < 2 * n;
             v[k] = r >= n;
             const int rr = live[k] ? (v[k] ? r - n : r) : 0;
@@ -418,14 +457,6 @@ pq_status launch_load(const pq_kv_cache &c, const LoadArgs &a, dim3 g, hipStream
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
-// log2 of the lanes that hold a row, 8 channels each.
-int row_lanes_log2(int dim)
-{
-    int l = 1;
-    while ((8 << l) < dim) ++l;
-    return l;
-}
-
 bool strides8(const int64_t *s, int n)
 {
     for (int i = 0; i < n; ++i)
@@ -467,6 +498,7 @@ pq_status pq_kv_append(const pq_kv_cache *cache, int dtype, int64_t tokens, cons
     if (q_heads && q == q_out && (q_token_stride != qo_token_stride || q_head_stride != qo_head_stride))
         return PQ_ERR_ARG;
     AppendArgs a = {};
+    a.lanes = RowLanes(c.dim);
     a.k = static_cast<uint8_t *>(c.k);
     a.v = static_cast<uint8_t *>(c.v);
     a.kp = static_cast<uint32_t *>(c.k_param);
@@ -498,10 +530,10 @@ pq_status pq_kv_append(const pq_kv_cache *cache, int dtype, int64_t tokens, cons
     a.rot = static_cast<int>(rot);
     a.half = layout == PQ_ROPE_HALF;
     a.q_heads = static_cast<int>(q_heads);
-    a.lanes_log2 = row_lanes_log2(c.dim);
     // Few tokens: a token's row groups go to several waves, as in the rotation.
-    const int side = 64 >> a.lanes_log2;
-    a.groups = 2 * ((c.heads + side - 1) / side) + (a.q_heads + side - 1) / side;
+    const int side = a.lanes.side;
+    a.kv_groups = (c.heads + side - 1) / side;
+    a.groups = 2 * a.kv_groups + (a.q_heads + side - 1) / side;
     int64_t slices = (2048 + tokens - 1) / tokens;
     if (slices > a.groups) slices = a.groups;
     a.slices = static_cast<int>(slices);
@@ -554,10 +586,10 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
     a.ko_hs = ko_head_stride;
     a.vo_ts = vo_token_stride;
     a.vo_hs = vo_head_stride;
-    a.lanes_log2 = row_lanes_log2(c.dim);
+    a.lanes = RowLanes(c.dim);
     // Few tokens: the heads of a token tile go to several blocks.
     const int64_t tiles = (tokens + kLoadTokens - 1) / kLoadTokens;
-    const int64_t per_round = kLoadRows * (256 >> a.lanes_log2);
+    const int64_t per_round = kLoadRows * (256 / a.lanes.n);
     const int64_t rounds = (2 * kLoadTokens * static_cast<int64_t>(c.heads) + per_round - 1) / per_round;
     int64_t slices = (1024 + tiles - 1) / tiles;
     if (slices > rounds) slices = rounds;

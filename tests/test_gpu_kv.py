@@ -241,3 +241,33 @@ def test_offsets_past_32_bits(pq, fmt):
         n, p = R.quantise(x.float(), bits)
         want = R.values(R.pack(n, bits), p, bits).float()
     assert torch.equal(out[0].cpu(), want) and torch.equal(out[1].cpu(), want)
+
+
+@pytest.mark.parametrize("dim", range(16, 257, 16))
+@pytest.mark.parametrize("fmt", ["kv8", "kv4"])
+def test_every_row_length(pq, fmt, dim):
+    """Rows side by side over a wave's lanes, whatever their length; the smallest and the largest value on each lane in turn."""
+    f, bits = FMT[fmt]
+    n, h, page = dim // 8, 7, 16
+    g = torch.Generator().manual_seed(dim)
+    k, v = (torch.randn(n, h, dim, generator=g).to(torch.bfloat16) for _ in range(2))
+    for i in range(n):
+        k[i, :, 8 * i + 3], k[i, :, (8 * i + 11) % dim] = -9.0, 11.0
+        v[i, :, (8 * i + 6) % dim], v[i, :, (8 * i - 4) % dim] = 12.0, -8.0
+    slots = torch.randperm(2 * page, generator=g)[:n]
+    cache = make_cache(pq, fmt, 2, page, h, dim)
+    pq.pq_kv_append(cache, k.to(DEV), v.to(DEV), slots.to(DEV))
+    check_cache(cache, fmt, bits, torch.bfloat16, slots, page, k.float(), v.float())
+    out = [Guarded((n, h, dim), torch.float32) for _ in range(2)]       # the first n slots, in order
+    pq.pq_kv_load(cache, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV), None,
+                  torch.tensor([0, n], dtype=torch.int32, device=DEV), out[0].t, out[1].t)
+    at = {int(s): i for i, s in enumerate(slots)}
+    for x, o in ((k, out[0]), (v, out[1])):
+        codes, par = R.quantise(x.float(), bits)
+        want = R.values(R.pack(codes, bits), par, bits)
+        mag = par.double()[..., 1:].abs() + par.double()[..., :1] * codes.double()
+        for t in range(n):
+            if t in at:             # one binary32 product and sum
+                err = (o.t[t].cpu().double() - want[at[t]]).abs()
+                assert (err <= 2.0 ** -23 * mag[at[t]]).all()
+        o.check("k_out / v_out")
