@@ -32,8 +32,8 @@ struct RowLanes {
 
 // ------------------------------------------------------------------ append
 
-// Row groups a wave has in flight: one, and six waves per SIMD (14 Ki tokens of
-// 30 heads of 80 channels 38 us; two groups 40, four 47).
+// Row groups a wave has in flight: one, and seven waves per SIMD (14 Ki tokens
+// of 30 heads of 80 channels, rows not yet packed: 38 us; two groups 40, four 47).
 constexpr int kAppendRows = 1;
 
 struct AppendArgs {
@@ -230,7 +230,7 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&n)[8])
 // waste six: 14 Ki tokens of 30 heads 38 us against 30); what kind of rows a group holds is the same
 // for the whole wave.  kAppendRows groups are
 // in flight, and the rotation's table values stay in registers over them.
-// What bounds it is vector instructions (some 900 a token at 30 heads of 80
+// What bounds it is vector instructions (some 600 a token at 30 heads of 80
 // channels), then the bytes.
 template <typename T, int FMT, typename CT>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
