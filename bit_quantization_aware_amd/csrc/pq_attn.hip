@@ -36,7 +36,7 @@
 // permutes.  No LDS and no cross-lane traffic in the loop but a maximum.
 //
 // Groups of few heads would leave most columns, and with them most lanes of
-// the softmax, without work.  With R = 2 the columns hold R copies of
+// the softmax, without work.  With R = 2 (4 bits) the columns hold R copies of
 // the group's heads; a wave takes R blocks of 32 tokens at a time and copy r
 // of the columns keeps block r only (its own m, l and o), so that every lane
 // works on tokens of its own: the softmax costs 1 / R.
@@ -936,13 +936,18 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
                   s_red[kWaves] + s_red[kWaves + 1] + s_red[kWaves + 2] + s_red[kWaves + 3], v);
 }
 
-// Rows of at most this many tokens are not split: one block takes such a row
-// in kWholeRow / 128 rounds, and a second launch would cost more.
-constexpr int kWholeRow = 512;
+// Rows of at most kWholeRow tokens are not split: one block takes such a row
+// in a few rounds, and a second launch would cost more (one bf16 sequence of
+// 1000 tokens 9.8 us against 11.4, of 2000 16.4 against 11.3; 64 of up to
+// 1000 in 8 bits, 512 rows, 21 against 29).  Where the rows alone fill the
+// chip that holds up to kWholeRowMany (512 rows of up to 2000 tokens 41 us
+// against 44; 128 rows 26 against 22).
+constexpr int kWholeRow = 1024, kWholeRowMany = 2048;
+constexpr int kManyRows = 256;      // one per CU
 
 // A call whose cache is larger than the memory-side cache (256 MB) finds
 // nothing of it there: its loads are non-temporal then (32 contexts of 16 Ki
-// bf16 tokens, 1.9 GB: 297 us against 326), but only where a row is whole
+// bf16 tokens, 1.9 GB: 293 us against 326), but only where a row is whole
 // 128-byte lines, else lines that two loads share are fetched twice (bf16 rows
 // of 80 channels: 108 us against 85).  A smaller cache may still lie there
 // from the call before (16 chats, 67 MB: 21 us against 17.5).
@@ -953,7 +958,7 @@ void launch_one(AttnArgs a, int64_t longest, hipStream_t s)
 {
     const int unit = 32 * R;
     const int64_t rows = static_cast<int64_t>(a.batch) * a.heads * a.gtiles;
-    if (longest <= kWholeRow) {
+    if (longest <= (rows >= kManyRows ? kWholeRowMany : kWholeRow)) {
         a.shares = 0;
         hipLaunchKernelGGL((k_attn_decode<QT, FMT, DP, R, NT>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a);
         return;
@@ -979,9 +984,12 @@ void launch_stream(const AttnArgs &a, int64_t longest, hipStream_t s)
 template <typename QT, int FMT, int DP>
 void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
-    // Two copies of the heads in the columns where the group leaves room.
-    // 16-bit rows take none: their bytes outlast the softmax.
-    if constexpr (FMT != PQ_KV_16) {
+    // Two copies of the heads in the columns where the group leaves room, for
+    // 4 bits (64 ragged contexts of 80 channels 38 us against 43, of 64
+    // channels 31 against 36, of 128 43.7 against 45) of up to 128 channels
+    // (of 256: 65 against 53).  More bytes a token outlast the
+    // softmax (8 bits, 128 channels: 72 us with two copies, 68 with one).
+    if constexpr (FMT == PQ_KV_4 && DP <= 128) {
         if (a.group <= 8) return launch_stream<QT, FMT, DP, 2>(a, longest, s);
     }
     launch_stream<QT, FMT, DP, 1>(a, longest, s);
