@@ -139,6 +139,27 @@ def test_split_rows(pq, fmt, lens):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("shape", [(1, 4, 80, 32), (2, 1, 128, 16), (1, 12, 128, 64), (1, 5, 256, 16), (2, 3, 48, 16), (1, 20, 80, 16)])
+def test_split_rows_of_every_shape(pq, shape, fmt):
+    """More tokens than one block takes, row ends inside a share and inside a tile; windows that start in the middle."""
+    heads, group, dim, page = shape
+    print(f"[attn split {shape} {fmt}]", flush=True)
+    c = Case(pq, fmt, [2300, 0, 1041, 2, 4111], heads, group, dim, page, torch.bfloat16, seed=dim)
+    c.check(*c.run(pq))
+    c.check(*c.run(pq, window=1900), window=1900)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("seqs", [127, 128])
+def test_unsplit_rows_where_there_are_many(pq, fmt, seqs):
+    """Rows of up to 1200 tokens, just too few and just enough of them for one block each."""
+    lens = [3 * i for i in range(seqs - 2)] + [1200, 0]
+    print(f"[attn many {fmt} {seqs}]", flush=True)
+    c = Case(pq, fmt, lens, 2, 2, 32, 16, torch.float16, seed=seqs)
+    c.check(*c.run(pq, max_len=1200))
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
 def test_token_major_pages_and_strided_q(pq, fmt):
     c = Case(pq, fmt, [77, 200], 3, 2, 64, 32, torch.bfloat16, token_major=True)
     fused = torch.randn(2, 12, 64).to(torch.bfloat16)
