@@ -211,7 +211,7 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 }
 
 // QT: type of q and out (and of a 16-bit cache).  FMT: cache format.  DP: dim
-// rounded up to 64, 128 or 256.  R: copies of the heads in the columns.  NT:
+// rounded up to 64, 96 (4 bits), 128 or 256.  R: copies of the heads in the columns.  NT:
 // the cache is read past the caches (launch_one).
 template <typename QT, int FMT, int DP, int R, bool NT>
 struct Attn {
@@ -225,12 +225,14 @@ struct Attn {
     static constexpr int kUnit = 32 * R;    // tokens of a step
     static constexpr int kCols = 16 / R;    // heads of a tile
     static constexpr int KS = DP / 32;      // k steps of the first product
-    static constexpr int E = DP / 16;       // channels of a lane in the second, in runs of kRun
+    static constexpr int VD = DP == 96 ? 128 : DP;  // channels of the second: a lane's E are whole words of codes
+    static constexpr int E = VD / 16;       // in runs of kRun
     static constexpr int kRun = kRaw && E == 16 ? 8 : E;    // (one 16-byte load each, side by side over the lanes)
     // Words of a lane per 16 tokens: K in KC runs of KW words (16-bit rows: 8
     // channels of step s at 32 s + 8 kb; codes: 16 channels at 64 c + 16 kb,
-    // which are steps 2c and 2c + 1), V in VW words per token.
-    static constexpr int KC = kRaw ? KS : KS / 2, KW = FMT == PQ_KV_4 ? 2 : 4;
+    // which are steps 2c and 2c + 1; of 96 the last 32: 8 at 64 + 8 kb), V in
+    // VW words per token.
+    static constexpr int KC = kRaw ? KS : (KS + 1) / 2, KW = FMT == PQ_KV_4 ? 2 : 4;
     static constexpr int VW = kRaw ? E / 2 : FMT == PQ_KV_8 ? E / 4 : E >= 8 ? E / 8 : 1;
     // The weights are scaled by 2^kShift, so that an f16 keeps 22 octaves
     // below the largest before it becomes subnormal; m may lag behind the
@@ -258,7 +260,8 @@ struct Attn {
         const uint16_t *row = a.q + b * a.q_bs + static_cast<int64_t>(kvh * a.group + (on ? g : 0)) * a.q_hs;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int d = kRaw ? 32 * s + 8 * kb() : 64 * (s >> 1) + 16 * kb() + 8 * (s & 1);
+            const bool single = kRaw || (KS % 2 && s == KS - 1);     // a step of its own, not half of a 64-channel run
+            const int d = single ? 32 * s + 8 * kb() : 64 * (s >> 1) + 16 * kb() + 8 * (s & 1);
             q[s] = u32x4{0, 0, 0, 0};
             if (on && d < a.dim) q[s] = *reinterpret_cast<const u32x4 *>(row + d);
         }
@@ -325,7 +328,7 @@ struct Attn {
 
     // Byte offsets of the lane's loads from a 16-token tile's first row, and
     // the tile's bytes.  Channels past dim: any, q is 0 there.
-    uint32_t k_off, k_last, v_off, v_step, v_second;
+    uint32_t k_off, k_last, k_half, v_off, v_step, v_second;
     int tile_bytes;
 
     __device__ __forceinline__ void set_offsets(const AttnArgs &a)
@@ -335,6 +338,7 @@ struct Attn {
         const uint32_t run = KW * 4, row_bytes = kRaw ? 2 * a.dim : FMT == PQ_KV_8 ? a.dim : a.dim / 2;
         k_off = row + kb() * run;
         k_last = row + row_bytes - run;
+        k_half = row + min(32 + 4 * kb(), static_cast<int>(row_bytes) - 4);      // 4 bits: 8 channels at 64 + 8 kb
         const uint32_t d = min(column() * kRun, a.dim - kRun);
         v_second = 2 * (min(128u + column() * kRun, static_cast<uint32_t>(a.dim - kRun)) - d);
         v_off = 4 * kb() * a.token_stride + (kRaw ? 2 * d : FMT == PQ_KV_8 ? d : d / 2);
@@ -348,6 +352,12 @@ struct Attn {
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
             const uint32_t at = min(k_off + c * (KW * 16), k_last);
+            if constexpr (DP == 96) {
+                if (c == KC - 1) {
+                    k[r][tile][c][0] = rows.load4(k_half);
+                    break;
+                }
+            }
             if constexpr (KW == 2) {
                 const u32x2 w = rows.template load8<NT>(at);
                 k[r][tile][c][0] = w[0];
@@ -397,7 +407,7 @@ struct Attn {
                 sum = mfma16<kF16>(u32x4{w[0], w[1], w[2], w[3]}, q[i], sum);
             } else {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                for (int s = 0; s < 2 && 2 * i + s < KS; ++s) {
                     u32x4 f;
                     if constexpr (FMT == PQ_KV_8) {
 #pragma unroll
@@ -599,7 +609,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
 {
     using A = Attn<QT, FMT, DP, R, NT>;
     constexpr int E = A::E, kUnit = A::kUnit, kCols = A::kCols;
-    constexpr int kPad = DP + 4;
+    constexpr int kPad = A::VD + 4;
     constexpr int kIds = 2 * R, kBatch = 64 / kIds;         // page ids of a step; steps whose ids a wave holds
     __shared__ int s_pre[kMaxBatch + 1], s_len[kMaxBatch];
     __shared__ int s_wsum[kWaves];
@@ -833,8 +843,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         __syncthreads();
         const bool opens = w.row0 + kRowCost >= begin, whole = opens && w.row0 + w.n <= end;
         const int slot = cut.slot(blockIdx.x, w.row0), hq0 = w.kvh * a.group + w.gt * 16;
-        for (int i = tid * 4; i < rows * DP; i += 1024) {
-            const int g = i / DP, d = i - g * DP;
+        for (int i = tid * 4; i < rows * A::VD; i += 1024) {
+            const int g = i / A::VD, d = i - g * A::VD;
             if (d >= a.dim) continue;
             const float M = top_of(g);
             float L = 0.f, Z = 0.f;
@@ -985,10 +995,10 @@ template <typename QT, int FMT, int DP>
 void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
     // Two copies of the heads in the columns where the group leaves room, for
-    // 4 bits (64 ragged contexts of 80 channels 38 us against 43, of 64
-    // channels 31 against 36, of 128 43.7 against 45) of up to 128 channels
-    // (of 256: 65 against 53).  More bytes a token outlast the
-    // softmax (8 bits, 128 channels: 72 us with two copies, 68 with one).
+    // 4 bits (64 ragged contexts of 64 channels 31 us against 36, of 128
+    // channels 43.7 against 45) of up to 128 channels (of 256: 65 against 53).
+    // More bytes a token outlast the softmax (8 bits, 128 channels: 72 us with
+    // two copies, 68 with one).
     if constexpr (FMT == PQ_KV_4 && DP <= 128) {
         if (a.group <= 8) return launch_stream<QT, FMT, DP, 2>(a, longest, s);
     }
@@ -998,8 +1008,14 @@ void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
 template <typename QT, int FMT>
 void launch_dim(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
-    if (a.dim <= 64) launch_copies<QT, FMT, 64>(a, longest, s);
-    else if (a.dim <= 128) launch_copies<QT, FMT, 128>(a, longest, s);
+    if (a.dim <= 64) return launch_copies<QT, FMT, 64>(a, longest, s);
+    // Vector instructions bound 4 bits: the first product leaves out the last
+    // 32 channels where it can (64 contexts of 80 channels 35.2 us against
+    // 37.1).  Other formats wait for their bytes.
+    if constexpr (FMT == PQ_KV_4) {
+        if (a.dim <= 96) return launch_copies<QT, FMT, 96>(a, longest, s);
+    }
+    if (a.dim <= 128) launch_copies<QT, FMT, 128>(a, longest, s);
     else launch_copies<QT, FMT, 256>(a, longest, s);
 }
 
