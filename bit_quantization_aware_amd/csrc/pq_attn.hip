@@ -70,7 +70,8 @@ constexpr int kMaxBatch = 1024;     // sequences of one launch (their step count
 constexpr int kMaxShares = 512;     // blocks of one launch: two per CU
 constexpr int kWaves = 4;
 // What a row costs a share beyond its steps (first loads, joining the waves,
-// a last round with idle waves), in steps of one wave.
+// a last round with idle waves), in steps of one wave.  64 ragged contexts of
+// 80 channels in 4 bits take 36.4 us with 8, 38.4 with 4, 36.8 with 12.
 constexpr int kRowCost = 8;
 
 struct AttnArgs {
