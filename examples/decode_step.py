@@ -1,7 +1,7 @@
 """Answering with a packed-weight attention layer, one token per sequence and
 step, on one GPU:
 
-    python examples/decode_step.py [--batch 8] [--steps 64] [--kv 16|8|4] [--graph]
+    python examples/decode_step.py [--batch 8] [--steps 512] [--kv 16|8|4] [--graph]
 
 A step is four calls: the packed projection to q, k and v (pq_gemm), the
 append that rotates q and k and writes k and v into the paged cache
@@ -125,7 +125,7 @@ def run(layer, steps, graph=False, seed=1):
 def main():
     ap = argparse.ArgumentParser(description="decode steps of a packed-weight attention layer")
     ap.add_argument("--batch", type=int, default=8)
-    ap.add_argument("--steps", type=int, default=64)
+    ap.add_argument("--steps", type=int, default=512)
     ap.add_argument("--kv", type=int, default=8, choices=sorted(FORMATS))
     ap.add_argument("--graph", action="store_true")
     args = ap.parse_args()
