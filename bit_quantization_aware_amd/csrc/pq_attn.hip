@@ -2,7 +2,7 @@
 // of one new token per sequence over a paged key-value cache of 16-, 8- or
 // 4-bit rows.
 //
-// Per query head, with x_t = scale log2(e) q . k^_t and a running reference m
+// Per query head, with x_t = scale log2(e) q . k^_t and a running whole-numbered reference m
 // (one pass over the cache):
 //   p_t = 2^(x_t - m),  l = sum p_t,  o = sum p_t v^_t,  out = o / l,
 // and whenever m grows by d, l and o are multiplied by 2^-d.
@@ -466,7 +466,7 @@ struct Attn {
     // to `ref` = m - kShift, which goes in with the constant of a token's row.
     __device__ __forceinline__ void softmax(float (&x)[8], unsigned seen, bool masked, u32x4 &hi, u32x4 &lo)
     {
-        float y[8];                 // x + log2 s_v (+ kBias): the exponent of the weight of the codes
+        float y[8];                 // x + log2 of s_v's size (+ kBias): the exponent of the weight of the codes
         float sv[8], zv[8];
         constexpr float kBias = kRaw ? 0.f : 127.f;
 #pragma unroll
@@ -480,8 +480,15 @@ struct Attn {
                 sv[i] = __builtin_bit_cast(float, vw << 16);
                 zv[i] = __builtin_bit_cast(float, vw & 0xFFFF0000u);
                 x[i] = __builtin_fmaf(sk, x[i] * c1, __builtin_fmaf(__builtin_fmaf(sk, mid, zk), c2, -ref));
+                // How large the row's values count: its scale; at least 2^-60,
+                // also where the row was never written and its scale is 0, and
+                // 2^-40 of its zero, so that neither p nor p z overflows.  (The
+                // elementwise maximum is one operation for three values; fmaxf
+                // brings its operands into canonical form first.)
+                const float size = __builtin_elementwise_maximum(
+                    __builtin_elementwise_maximum(fabsf(sv[i]), fabsf(zv[i]) * 0x1p-40f), kMinKvScale);
                 // the bits of a positive float are 2^23 (127 + log2) to within 0.09 octaves
-                y[i] = __builtin_fmaf(static_cast<float>(vw << 16), 0x1p-23f, x[i]);
+                y[i] = __builtin_fmaf(static_cast<float>(__builtin_bit_cast(uint32_t, size)), 0x1p-23f, x[i]);
             }
         }
         if (masked) {
@@ -503,7 +510,9 @@ struct Attn {
         }
         const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
         if (__ballot(top > limit)) {                // also the first step: limit is -inf
-            const float mn = fmaxf(m, column_max(top) + (ref - kBias));
+            // A whole number, so that the shift and the factors of l and o are
+            // exact, however far below 0 rows of the smallest scale bring it.
+            const float mn = floorf(fmaxf(m, column_max(top) + (ref - kBias)));
             const float f = m == mn ? 1.f : exp2_fast(m - mn);
             const float next = mn == -__builtin_inff() ? ref : mn - kShift, by = ref - next;
             m = mn;
@@ -591,9 +600,12 @@ __device__ __forceinline__ void write_out(const AttnArgs &a, int b, int hq, int 
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     *reinterpret_cast<u32x2 *>(a.out + b * a.out_bs + hq * a.out_hs + d) =
         u32x2{pack16<QT>(v[0] * inv, v[1] * inv), pack16<QT>(v[2] * inv, v[3] * inv)};
+    // M is a whole number, the exponent of L joins it exactly
     if (d == 0 && a.lse)
         a.lse[static_cast<int64_t>(b) * a.q_heads + hq] =
-            L == 0.f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+            L == 0.f ? -__builtin_inff()
+                     : (M + static_cast<float>(__builtin_amdgcn_frexp_expf(L)) +
+                        __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(L))) * 0.69314718055994531f;
 }
 
 // A row (sequence, cache head, head tile) of a share, as its waves see it.
@@ -812,8 +824,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         if (w.count > 0 && follows) st.load_q(a, next.b, next.kvh, next.gt);
         ready = w.count > 0 && follows && next.count > 0;
         // join the waves and the copies of the columns
-        // the weights' scale 2^kShift goes out of the sums before l meets a
-        // logarithm, whose rounding would else be that of a number 7 larger
+        // the weights' scale 2^kShift goes out of the sums
         const float l_all = column_sum(st.l) * A::kUnscale, z_all = column_sum(st.zsum) * A::kUnscale;
         __syncthreads();                            // the last row's s_m and s_o have been read
         if (kb == 0) {

@@ -605,7 +605,9 @@ pq_status pq_rope(int dtype, int64_t tokens, int64_t heads, int64_t dim, int64_t
  *   z = bf16(min x),  s = max(bf16((max x - min x) fl32(1 / Q)), 2^-60),
  *   n = clamp(rint((x - z) r), 0, Q),  r = fl32(1 / s),
  * fp32 throughout, one rounding an operation, rint to even.  A row that holds
- * a NaN is stored with a NaN zero and reads back as NaN. */
+ * a NaN is stored with a NaN zero and reads back as NaN; so does a row whose
+ * range is not finite.  Rows of zero bytes, which nothing was written to, are
+ * rows of zeros; pairs from elsewhere may hold any s and z. */
 #define PQ_KV_16 0
 #define PQ_KV_8 1
 #define PQ_KV_4 2
