@@ -328,7 +328,10 @@ struct Attn {
     }
 
     // Byte offsets of the lane's loads from a 16-token tile's first row, and
-    // the tile's bytes.  Channels past dim: any, q is 0 there.
+    // the tile's bytes.  Channels past dim meet a q of 0: any codes do there,
+    // but 16-bit values may be infinite, so those come as 0, from an offset
+    // that lies behind every tile (a buffer load gives 0 there).
+    static constexpr uint32_t kNowhere = 0x80000000u;
     uint32_t k_off, k_last, k_half, v_off, v_step, v_second;
     int tile_bytes;
 
@@ -352,7 +355,9 @@ struct Attn {
         const Resource rows(tile_row, tile_bytes);
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-            const uint32_t at = min(k_off + c * (KW * 16), k_last);
+            uint32_t at = k_off + c * (KW * 16);
+            if constexpr (!kRaw) at = min(at, k_last);
+            else if (DP == 64 || c >= KC / 2) at = at <= k_last ? at : kNowhere;    // dim > DP / 2 but for DP = 64
             if constexpr (DP == 96) {
                 if (c == KC - 1) {
                     k[r][tile][c][0] = rows.load4(k_half);

@@ -94,6 +94,20 @@ def test_large_constant_values(pq, fmt, size):
     c.check(*c.run(pq))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 128, 192, 208, 256])
+def test_keys_with_an_infinity(pq, dim, dtype):
+    """A score of minus infinity is a weight of 0, whatever channel of the key it comes from."""
+    page, n = 16, 70
+    for channel in sorted({0, dim // 2 - 1, dim - 8, dim - 1}):
+        c = Case(pq, "kv16", [n, 9], 2, 3, dim, page, dtype, seed=channel)
+        c.q[..., channel] = -1.0
+        for t in (0, 37, 69):
+            at = int(c.table[0, t // page])
+            c.cache.tensors[0][at, :, t % page, channel] = float("inf")
+        c.check(*c.run(pq), hidden={(0, t) for t in (0, 37, 69)})
+
+
 @pytest.mark.parametrize("fmt", ["kv8", "kv4"])
 @pytest.mark.parametrize("bad", ["inf", "-inf", "range"])
 def test_rows_without_a_finite_scale(pq, fmt, bad):
