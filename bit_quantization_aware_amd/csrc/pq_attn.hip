@@ -64,6 +64,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxBatch = 1024;     // sequences of one launch (their step counts sit in LDS)
@@ -100,6 +101,12 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// What sums with the reference `from` are multiplied by to have the reference
+// `to`; not 0, so that an infinite sum stays one.
+__device__ __forceinline__ float rescale(float from, float to)
+{
+    return from == to ? 1.f : __builtin_elementwise_maximum(exp2_fast(from - to), 0x1p-126f);
+}
 
 // Attended range of a sequence, its first token rounded down to a 16-token
 // tile: pages are whole numbers of those.
@@ -218,11 +225,15 @@ template <typename QT, int FMT, int DP, int R, bool NT>
 struct Attn {
     static constexpr bool kRaw = FMT == PQ_KV_16;
     static constexpr bool kF16 = !kRaw || __is_same(QT, f16_t);   // operand type of both products
-    using OT = typename std::conditional<kF16, f16_t, bf16_t>::type;
-    // The weights p (or p s) enter the second product as two 16-bit values,
-    // the second carrying the first one's remainder: rounded to one (2^-9
-    // off in bf16, 2^-12 in f16) they would add as much to the output's error
-    // as its own rounding.  The matrix unit has the room.
+    // The weights p (or p s) enter the second product as several 16-bit values,
+    // each carrying the remainder of the one before: rounded to one (2^-9 off
+    // in bf16, 2^-12 in f16) they would add as much to the output's error as
+    // its own rounding.  Two hold 22 bits in f16, three hold all 24 in bf16.
+    // The matrix unit has the room.  Of 16-bit rows they are cut off, never
+    // rounded up, and not 0 where the weight is not: an infinite value then
+    // meets no 0 and no negative remainder, and the sum is infinite too.  (An
+    // f16 weight below 2^-24 has no such value: infinity by 0 is NaN there.)
+    static constexpr int kPieces = kF16 ? 2 : 3;
     static constexpr int kUnit = 32 * R;    // tokens of a step
     static constexpr int kCols = 16 / R;    // heads of a tile
     static constexpr int KS = DP / 32;      // k steps of the first product
@@ -469,7 +480,7 @@ struct Attn {
     // Scores to weights, as operands.  `seen`: bit i for token 4 kb + i of the
     // own block's first tile, bit 4 + i of its second.  Everything is relative
     // to `ref` = m - kShift, which goes in with the constant of a token's row.
-    __device__ __forceinline__ void softmax(float (&x)[8], unsigned seen, bool masked, u32x4 &hi, u32x4 &lo)
+    __device__ __forceinline__ void softmax(float (&x)[8], unsigned seen, bool masked, u32x4 (&weights)[kPieces])
     {
         float y[8];                 // x + log2 of s_v's size (+ kBias): the exponent of the weight of the codes
         float sv[8], zv[8];
@@ -518,7 +529,7 @@ struct Attn {
             // A whole number, so that the shift and the factors of l and o are
             // exact, however far below 0 rows of the smallest scale bring it.
             const float mn = floorf(fmaxf(m, column_max(top) + (ref - kBias)));
-            const float f = m == mn ? 1.f : exp2_fast(m - mn);
+            const float f = rescale(m, mn);
             const float next = mn == -__builtin_inff() ? ref : mn - kShift, by = ref - next;
             m = mn;
             ref = next;
@@ -546,35 +557,44 @@ struct Attn {
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // f16: the first is cut off, in one operation for both; the second has what is left
-            if constexpr (kF16) hi[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(w[2 * i], w[2 * i + 1]));
-            else hi[i] = pack16<OT>(w[2 * i], w[2 * i + 1]);
-            float h0, h1;
-            unpack16<OT>(hi[i], h0, h1);
             if constexpr (kF16) {
+                // the first is cut off, in one operation for both; the second has what is left
+                const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(w[2 * i], w[2 * i + 1]));
+                float h0, h1;
+                unpack16<f16_t>(hi, h0, h1);
                 // written as multiply-adds: one operation takes the f16, subtracts and rounds to f16
                 const f16x2_t r = {static_cast<_Float16>(__builtin_fmaf(-h0, 1.f, w[2 * i])),
                                    static_cast<_Float16>(__builtin_fmaf(-h1, 1.f, w[2 * i + 1]))};
-                lo[i] = __builtin_bit_cast(uint32_t, r);
+                u16x2_t lo = __builtin_bit_cast(u16x2_t, r);
+                if constexpr (kRaw)                 // at least 2^-24 beside a first that is not 0
+                    lo = __builtin_elementwise_max(lo, __builtin_elementwise_min(__builtin_bit_cast(u16x2_t, hi), u16x2_t{1, 1}));
+                weights[0][i] = hi;
+                weights[1][i] = __builtin_bit_cast(uint32_t, lo);
             } else {
-                lo[i] = pack16<OT>(w[2 * i] - h0, w[2 * i + 1] - h1);
+                float a = w[2 * i], b = w[2 * i + 1];
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) {
+                    a = __builtin_elementwise_maximum(a, 0x1p-126f);
+                    b = __builtin_elementwise_maximum(b, 0x1p-126f);
+                    const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
+                    weights[n][i] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
+                    a -= __builtin_bit_cast(float, ab & 0xFFFF0000u);
+                    b -= __builtin_bit_cast(float, bb & 0xFFFF0000u);
+                }
             }
         }
     }
 
-    __device__ __forceinline__ void second_product(const u32x4 &hi, const u32x4 &lo)
+    __device__ __forceinline__ void second_product(const u32x4 (&weights)[kPieces])
     {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            u32x4 h = hi, w = lo;
-            if constexpr (R > 1) {
-                const bool own = copy() == r;
+            u32x4 w[kPieces];
+            const bool own = R == 1 || copy() == r;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = own ? hi[i] : 0u;
-                    w[i] = own ? lo[i] : 0u;
-                }
-            }
+            for (int n = 0; n < kPieces; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[n][i] = own ? weights[n][i] : 0u;
             // four channels at a time, so that no product waits for the one before
 #pragma unroll
             for (int e0 = 0; e0 < E; e0 += 4) {
@@ -582,10 +602,12 @@ struct Attn {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     f[e] = v_operand(r, e0 + e);
-                    o[e0 + e] = mfma16<kF16>(f[e], h, o[e0 + e]);
+                    o[e0 + e] = mfma16<kF16>(f[e], w[0], o[e0 + e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e0 + e] = mfma16<kF16>(f[e], w, o[e0 + e]);
+                for (int n = 1; n < kPieces; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e0 + e] = mfma16<kF16>(f[e], w[n], o[e0 + e]);
             }
         }
     }
@@ -819,10 +841,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
                     if (valid(id) && u >= w.r.first && u < w.r.len) seen |= 1u << e;
                 }
             }
-            u32x4 hi, lo;
-            st.softmax(x, seen, masked, hi, lo);
+            u32x4 weights[A::kPieces];
+            st.softmax(x, seen, masked, weights);
             load_pairs(kvh, then);
-            st.second_product(hi, lo);
+            st.second_product(weights);
             load_values();
             now = then;
         }
@@ -848,7 +870,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
             return M;
         };
         if (g_own < rows) {
-            const float M = top_of(g_own), f = (st.m == M ? 1.f : exp2_fast(st.m - M)) * A::kOUnit;
+            const float M = top_of(g_own), f = rescale(st.m, M) * A::kOUnit;
             float *so = s_o + (wave * 16 + column) * kPad;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -870,7 +892,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
 #pragma unroll
                 for (int c = 0; c < R; ++c) {
                     const int col = c * kCols + g;
-                    const float fw = s_m[u][col] == M ? 1.f : exp2_fast(s_m[u][col] - M);
+                    const float fw = rescale(s_m[u][col], M);
                     L += s_l[u][col] * fw;
                     Z += s_z[u][col] * fw;
                     v += *reinterpret_cast<const f32x4 *>(s_o + (u * 16 + col) * kPad + d);
@@ -938,7 +960,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
             float L = 0.f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float f = ml[k][0] == M ? 1.f : exp2_fast(ml[k][0] - M);
+                const float f = rescale(ml[k][0], M);
                 if (tid + 256 * k < n) s_w[tid + 256 * k] = f;
                 L = __builtin_fmaf(ml[k][1], f, L);
             }

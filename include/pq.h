@@ -680,7 +680,12 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
  * pq_attn_decode -- attention of one new token per sequence over the cache:
  *   x_t = scale * q . k^_t,   t in [max(0, len - window), len)
  *   out = sum_t softmax(x)_t v^_t,   lse = ln sum_t exp x_t
- * in fp32; query head h reads cache head h / (q_heads / heads).
+ * with sums, maximum and weights in fp32; query head h reads cache head
+ * h / (q_heads / heads).  The matrix unit takes the weights in 16-bit pieces:
+ * all 24 bits over a bf16 cache, the upper 22 over the others.  A score of
+ * -inf has weight 0.  An infinite value of an attended token makes its channel
+ * of out infinite; two of opposite signs give NaN, and so may one in an f16
+ * cache whose weight is below 2^-30 of the largest.
  *   q, out       [batch, q_heads, dim] of q_dtype (PQ_BF16 or PQ_F16; the
  *                cache's dtype if that is PQ_KV_16), 16-byte aligned, strides
  *                (elements) multiples of 8

@@ -108,6 +108,36 @@ def test_keys_with_an_infinity(pq, dim, dtype):
         c.check(*c.run(pq), hidden={(0, t) for t in (0, 37, 69)})
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dim", [64, 80, 192])
+@pytest.mark.parametrize("n", [33, 700, 3000])
+def test_values_with_an_infinity(pq, n, dim, dtype):
+    """An attended infinity is the sum's: with its sign, in its channel and nowhere else; two of opposite signs are NaN."""
+    page, inf = 16, float("inf")
+    c = Case(pq, "kv16", [n], 2, 3, dim, page, dtype, seed=n)
+    put = {1: [(n // 2, inf)], 9: [(0, -inf)], dim - 2: [(3, inf), (n - 1, -inf)], dim - 1: [(t, -inf) for t in range(5, n, 7)]}
+    for channel, places in put.items():
+        for t, x in places:
+            c.cache.tensors[1][int(c.table[0, t // page]), :, t % page, channel] = x
+    out, lse = c.run(pq)
+    assert bool((out[0, :, 1] == inf).all()) and bool((out[0, :, 9] == -inf).all())
+    assert bool(out[0, :, dim - 2].isnan().all()) and bool((out[0, :, dim - 1] == -inf).all())
+    for channel in put:                             # the others are what they are without
+        c.v[0][:, :, channel] = c.mag[1][0][:, :, channel] = 0
+        out[0, :, channel] = 0
+    c.check(out, lse)
+
+
+def test_values_with_an_infinity_and_little_weight(pq):
+    """bf16 keeps the infinity of a token whose weight is too small for binary32."""
+    page, n, d, inf = 16, 400, 128, float("inf")
+    c = Case(pq, "kv16", [n], 2, 4, d, page, torch.bfloat16, gain=30.0)
+    for t in range(n):
+        c.cache.tensors[1][int(c.table[0, t // page]), :, t % page, t % d] = inf
+    out, _ = c.run(pq, scale=0.5)
+    assert bool((out == inf).all())
+
+
 @pytest.mark.parametrize("fmt", ["kv8", "kv4"])
 @pytest.mark.parametrize("bad", ["inf", "-inf", "range"])
 def test_rows_without_a_finite_scale(pq, fmt, bad):
