@@ -7,6 +7,7 @@ computation runs in libpq's HIP kernels.  Importing this module loads
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -166,6 +167,17 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _memory_of(stream):
+    """Where a buffer that a call on `stream` makes for itself comes from: the
+    launch stream's own memory.  A block of the caller's current stream may
+    have been freed there with work still queued on it, and nothing makes the
+    launch stream wait for that work; one of the launch stream is handed out
+    again only behind the call, in the stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _check(rc: int, fn: str) -> None:
     if rc != 0:
         raise PQError(rc, fn)
@@ -229,17 +241,13 @@ def gemm_workspace(mode: int, M: int, N: int, K: int, device="cuda") -> Optional
 
 def _ws(mode, M, N, K, X, workspace, stream):
     """(pointer, size, tensor) of the caller's workspace, or of one allocated
-    here from torch's caching allocator.  A buffer allocated here is marked
-    as used by the launch stream, so torch hands it out again only after the
-    GEMM on that stream is done with it."""
+    here from torch's caching allocator, out of the launch stream's memory."""
     if workspace is None:
         dev = X.device if isinstance(X, torch.Tensor) else "cuda"
-        workspace = gemm_workspace(mode, M, N, K, dev)
+        with _memory_of(stream):
+            workspace = gemm_workspace(mode, M, N, K, dev)
         if workspace is None:
             return None, 0, None
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-            workspace.record_stream(s)
     if isinstance(workspace, tuple):        # (pointer, bytes) from a caller that keeps its own buffer
         return workspace[0], int(workspace[1]), None
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -417,9 +425,10 @@ def pq_rope_table(max_pos, rot, base=10000.0, table=None, scaling: Optional[pq_r
                   device="cuda") -> torch.Tensor:
     """The (cos, sin) rows of positions 0 .. max_pos - 1: f32 [max_pos, rot / 2, 2], made here if not given."""
     if table is None:
-        table = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device)
-        if stream is not None:
-            table.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        with _memory_of(stream):
+            table = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device)
+        if stream is not None:          # the caller goes on to use it there
+            table.record_stream(torch.cuda.current_stream())
     _check(lib.pq_rope_table(max_pos, rot, float(base), ctypes.addressof(scaling) if scaling is not None else None,
                              _array(table, torch.float32, max_pos * rot, "table"), _stream(stream)), "pq_rope_table")
     return table
@@ -596,9 +605,8 @@ def pq_attn_decode(cache: KVCache, q, block_table, lens, out, lse=None, scale=No
     ot, oh = _rows(out, "out")
     bp, bs, bn = _block_table(block_table, batch)
     if workspace is None:
-        workspace = attn_workspace(cache, batch, q_heads, q.device)
-        if stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        with _memory_of(stream):
+            workspace = attn_workspace(cache, batch, q_heads, q.device)
     rc = lib.pq_attn_decode(cache.ptr, _dtype(q, "q"), batch, q_heads, q.data_ptr(), qt, qh, bp, bs, bn,
                             _array(lens, torch.int32, batch, "lens"), dim ** -0.5 if scale is None else scale, window,
                             max_len, out.data_ptr(), ot, oh,
