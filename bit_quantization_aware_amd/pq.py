@@ -523,8 +523,8 @@ class KVCache:
 
 def pq_kv_append(cache: KVCache, k, v, slots, positions=None, table=None, layout=PQ_ROPE_HALF, q=None, q_out=None,
                  stream=None) -> None:
-    """Write k, v [tokens, heads, dim] into the cache at slots; with a table k is rotated on the way, and q
-    [tokens, q_heads, dim] is rotated into q_out (None: in place) in the same launch."""
+    """Write k, v [tokens, heads, dim] into the cache at slots, each token at its own (padding: -1); with a table k
+    is rotated on the way, and q [tokens, q_heads, dim] is rotated into q_out (None: in place) in the same launch."""
     n, heads, dim = shape = k.shape
     kt, kh = _rows(k, "k")
     vt, vh = _rows(v, "v")

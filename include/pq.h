@@ -641,8 +641,10 @@ int64_t pq_kv_row_bytes(int format, int64_t dim);
  *   dtype      of k, v, q and q_out: PQ_F32, PQ_BF16 or PQ_F16
  *   k, v       in [tokens, heads, dim], strides in elements
  *   slots      in [tokens] int64: page * page_size + offset.  A slot below 0
- *              or past the cache is skipped (padding).  Two tokens with the
- *              same slot: either may stay
+ *              or past the cache is skipped: padding has to use one, since
+ *              the tokens of a call are written side by side.  Where two have
+ *              the same slot, its rows may mix them (the codes of one with the
+ *              scale of the other)
  *   table      (with positions, max_pos, rot, layout, as pq_rope) rotates k
  *              in fp32 before it is stored, so that it is rounded once; NULL
  *              stores k as it is
