@@ -1146,7 +1146,8 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     // lens past max_len count as max_len: rows are then known to be short
     if (max_len > 0 && max_len < a.max_tokens) a.max_tokens = static_cast<int>(max_len);
     int64_t longest = a.max_tokens;
-    if (window > 0 && longest > window + 15) longest = window + 15;   // its first tile may start 15 tokens early
+    // its first tile may start 15 tokens early
+    if (a.window > 0 && longest > int64_t(a.window) + 15) longest = int64_t(a.window) + 15;
     // the kernel counts steps of at least 32 tokens and row costs in 32 bits
     const int64_t row_steps = (static_cast<int64_t>(a.max_tokens) + 31) / 32 + 1 + kRowCost;
     int64_t most = INT32_MAX / (row_steps * c.heads * a.gtiles);

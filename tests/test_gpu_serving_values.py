@@ -138,6 +138,22 @@ def test_values_with_an_infinity_and_little_weight(pq):
     assert bool((out == inf).all())
 
 
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_the_longest_window(pq, fmt):
+    """A window of 2^63 - 1 tokens is no window: the row is split over the blocks as without one."""
+    c = Case(pq, fmt, [5000], 1, 4, 64, 16, torch.bfloat16)
+    table, lens = c.table.to(DEV), torch.tensor(c.lens, dtype=torch.int32, device=DEV)
+    size = pq.pq_attn_decode_workspace_bytes(c.cache, 1, 4)
+    got = []
+    for window in (0, 2 ** 63 - 1, 2 ** 31):
+        out, ws = torch.empty(1, 4, 64, dtype=torch.bfloat16, device=DEV), torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV)
+        pq.pq_attn_decode(c.cache, c.q.to(DEV), table, lens, out, window=window, workspace=ws)
+        got.append((out, ws))
+    for out, ws in got[1:]:
+        assert torch.equal(out, got[0][0])
+        assert bool((ws != 0xA5).any()), "not split"
+
+
 @pytest.mark.parametrize("fmt", ["kv8", "kv4"])
 @pytest.mark.parametrize("bad", ["inf", "-inf", "range"])
 def test_rows_without_a_finite_scale(pq, fmt, bad):
