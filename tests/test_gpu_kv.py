@@ -271,3 +271,31 @@ def test_every_row_length(pq, fmt, dim):
                 err = (o.t[t].cpu().double() - want[at[t]]).abs()
                 assert (err <= 2.0 ** -23 * mag[at[t]]).all()
         o.check("k_out / v_out")
+
+
+@pytest.mark.parametrize("dim", range(16, 257, 16))
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_every_row_length_reads_back(pq, fmt, dim):
+    """Every token written is read and compared, wherever its slot is."""
+    f, bits = FMT[fmt]
+    n, h, page = 32, 5, 16
+    g = torch.Generator().manual_seed(dim + 1)
+    k, v = (torch.randn(n, h, dim, generator=g).to(torch.bfloat16) for _ in range(2))
+    slots = torch.randperm(2 * page, generator=g)
+    cache = make_cache(pq, fmt, 2, page, h, dim)
+    pq.pq_kv_append(cache, k.to(DEV), v.to(DEV), slots.to(DEV))
+    out = [Guarded((n, h, dim), torch.float32) for _ in range(2)]
+    pq.pq_kv_load(cache, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV), None,
+                  torch.tensor([0, n], dtype=torch.int32, device=DEV), out[0].t, out[1].t)
+    torch.cuda.synchronize()
+    for x, o in ((k, out[0]), (v, out[1])):
+        o.check("k_out / v_out")
+        got = o.t.cpu()[slots].double()             # slot s is row s of the output
+        assert got.shape[0] == n
+        if bits == 16:
+            assert torch.equal(got, x.double())
+            continue
+        codes, par = R.quantise(x.float(), bits)
+        want = R.values(R.pack(codes, bits), par, bits)
+        mag = par.double()[..., 1:].abs() + par.double()[..., :1] * codes.double()
+        assert bool(((got - want).abs() <= 2.0 ** -23 * mag).all())       # one binary32 product and sum
