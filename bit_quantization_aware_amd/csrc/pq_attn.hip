@@ -1083,7 +1083,7 @@ extern "C" {
 int64_t pq_attn_decode_workspace_bytes(const pq_kv_cache *cache, int64_t batch, int64_t q_heads)
 {
     using namespace pq;
-    if (kv_cache_status(cache) != PQ_OK || batch < 0 || q_heads < 1 || q_heads % cache->heads) return -1;
+    if (kv_cache_status(cache) != PQ_OK || batch < 0 || q_heads < 1 || q_heads > 65535 || q_heads % cache->heads) return -1;
     if (batch == 0) return 0;
     return (attn_workspace(*cache, batch, static_cast<int>(q_heads / cache->heads)) + 15) / 16 * 16;
 }
@@ -1152,6 +1152,7 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
     const int64_t row_steps = (static_cast<int64_t>(a.max_tokens) + 31) / 32 + 1 + kRowCost;
     int64_t most = INT32_MAX / (row_steps * c.heads * a.gtiles);
     if (most < 1) return PQ_ERR_SHAPE;
+    if (most > kMaxBlocks / q_heads) most = kMaxBlocks / q_heads;     // a block per query head joins the shares
     if (most > kMaxBatch) most = kMaxBatch;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     for (int64_t b0 = 0; b0 < batch; b0 += most) {

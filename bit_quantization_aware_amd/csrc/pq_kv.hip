@@ -329,7 +329,7 @@ template <typename T>
 pq_status launch_append(const pq_kv_cache &c, const AppendArgs &a, hipStream_t s)
 {
     const int64_t blocks = (a.tokens + 3) / 4;
-    if (blocks > INT32_MAX) return PQ_ERR_SHAPE;
+    if (blocks > kMaxBlocks) return PQ_ERR_SHAPE;
     const dim3 g(static_cast<unsigned>(blocks), static_cast<unsigned>(a.slices)), b(256);
     if (c.format == PQ_KV_8) hipLaunchKernelGGL((k_kv_append<T, PQ_KV_8, bf16_t>), g, b, 0, s, a);
     else if (c.format == PQ_KV_4) hipLaunchKernelGGL((k_kv_append<T, PQ_KV_4, bf16_t>), g, b, 0, s, a);
@@ -600,7 +600,7 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
     int64_t slices = (1024 + tiles - 1) / tiles;
     if (slices > rounds) slices = rounds;
     a.slices = static_cast<int>(slices);
-    if (tiles > INT32_MAX) return PQ_ERR_SHAPE;
+    if (tiles > kMaxBlocks) return PQ_ERR_SHAPE;
     const dim3 blocks(static_cast<unsigned>(tiles), static_cast<unsigned>(slices));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == PQ_F32) return launch_load<float>(c, a, blocks, s);

@@ -141,6 +141,9 @@ __device__ __forceinline__ void store_f32(T *p, const float (&x)[N])
     }
 }
 
+// Blocks of 256 threads of one launch: a grid's threads are counted in 32 bits.
+constexpr int64_t kMaxBlocks = ((int64_t(1) << 32) - 1) / 256;
+
 // Smallest scale of a quantised row, 2^-60: a constant row then has a scale
 // whose reciprocal and whose logarithm are finite.
 constexpr float kMinKvScale = 0x1p-60f;

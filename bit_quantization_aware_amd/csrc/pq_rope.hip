@@ -167,15 +167,14 @@ pq_status launch_rope(RopeArgs a, bool in_place, hipStream_t s)
     // heads 3.2 us, unsliced 4.1).
     int64_t slices = (2048 + a.tokens - 1) / a.tokens;
     if (slices > rounds) slices = rounds;
-    if (slices > 65535) slices = 65535;             // a grid's second dimension
     a.slices = static_cast<int>(slices);
     const int64_t blocks = (a.tokens + 3) / 4;
-    if (blocks > INT32_MAX) return PQ_ERR_SHAPE;
+    if (blocks > kMaxBlocks) return PQ_ERR_SHAPE;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(slices));
     // Past the memory-side cache (256 MB) the rotated heads are not written
     // into the caches: the 8 x 2048 batch (340 MB) 60 us against 63.  A smaller
     // result may be found there by its reader: 66 MB in fp32 13.5 us against 17.6.
-    if (a.tokens * a.heads * a.dim * 2 * static_cast<int64_t>(sizeof(T)) > (int64_t(256) << 20))
+    if (static_cast<double>(a.tokens) * a.heads * a.dim * 2 * sizeof(T) > 0x1p28)
         hipLaunchKernelGGL((k_rope<T, VP, true>), grid, dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((k_rope<T, VP, false>), grid, dim3(256), 0, s, a);
@@ -238,7 +237,7 @@ pq_status pq_rope_table(int64_t max_pos, int64_t rot, double base, const pq_rope
     if (!table) return PQ_ERR_NULL;
     if (!aligned16(table)) return PQ_ERR_ALIGN;
     const int64_t blocks = (max_pos * t.pairs + 255) / 256;
-    if (blocks > INT32_MAX) return PQ_ERR_SHAPE;
+    if (blocks > kMaxBlocks) return PQ_ERR_SHAPE;
     hipLaunchKernelGGL(k_rope_table, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), t);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
@@ -252,7 +251,8 @@ pq_status pq_rope(int dtype, int64_t tokens, int64_t heads, int64_t dim, int64_t
     using namespace pq;
     const int size = dtype_bytes(dtype);
     if (!size || (layout != PQ_ROPE_HALF && layout != PQ_ROPE_INTERLEAVED)) return PQ_ERR_MODE;
-    if (tokens < 0 || heads < 0 || heads > INT32_MAX || dim < 1 || dim > 1024 || rot < 0 || rot > dim || rot % 2)
+    // the kernel steps through the heads in 32 bits, up to 2^19 at a time
+    if (tokens < 0 || heads < 0 || heads > (1 << 30) || dim < 1 || dim > 1024 || rot < 0 || rot > dim || rot % 2)
         return PQ_ERR_SHAPE;
     if (max_pos < 0 || max_pos > INT32_MAX) return PQ_ERR_SHAPE;
     if (tokens == 0 || heads == 0) return PQ_OK;

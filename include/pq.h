@@ -571,7 +571,8 @@ typedef struct pq_rope_scaling {
 /* pq_rope_table -- the (cos, sin) rows of positions 0 .. max_pos - 1, made
  * once per model: table [max_pos, rot / 2, 2] fp32, each value rounded once
  * from binary64.
- *   rot      even, 2 .. 1024;  max_pos 0 .. 2^31 - 1;  base > 1
+ *   rot      even, 2 .. 1024;  max_pos 0 .. 2^31 - 1, at most 2^33 - 512
+ *            values in all;  base > 1
  *   scaling  host pointer read during the call, or NULL for PQ_ROPE_PLAIN
  * An unknown kind -> PQ_ERR_MODE; base or a scaling value out of range (or
  * not finite) -> PQ_ERR_ARG. */
@@ -585,6 +586,7 @@ pq_status pq_rope_table(int64_t max_pos, int64_t rot, double base, const pq_rope
  * channels are copied.  `inverse` != 0 takes -sin: the transposed rotation,
  * which is the gradient of the forward call.
  *   dtype      PQ_F32, PQ_BF16 or PQ_F16, of x and y
+ *   tokens     at most 2^26 - 4;  heads at most 2^30
  *   dim        1 .. 1024;  rot even, 0 .. dim
  *   strides    elements between tokens and between heads, any value
  *   positions  in [tokens] int32.  A negative one (padding) leaves the row as
@@ -639,6 +641,7 @@ int64_t pq_kv_row_bytes(int format, int64_t dim);
  * the keys (and the queries) on the way.
  *   cache      host pointer read during the call
  *   dtype      of k, v, q and q_out: PQ_F32, PQ_BF16 or PQ_F16
+ *   tokens     at most 2^26 - 4;  q_heads at most 65535
  *   k, v       in [tokens, heads, dim], strides in elements
  *   slots      in [tokens] int64: page * page_size + offset.  A slot below 0
  *              or past the cache is skipped: padding has to use one, since
@@ -667,7 +670,8 @@ pq_status pq_kv_append(const pq_kv_cache *cache, int dtype, int64_t tokens, cons
  *   dtype        of k_out and v_out (x^ in fp32, rounded once)
  *   starts       in [batch] int32, or NULL for 0
  *   cu           in [batch + 1] int32, not decreasing, cu[0] = 0
- *   tokens       rows of k_out and v_out (cu[batch], known to the caller)
+ *   tokens       rows of k_out and v_out (cu[batch], known to the caller), at
+ *                most 2^28 - 16
  *   max_pages    columns of block_table.  A token past them, a page id outside
  *                the cache and rows past cu[batch] read as 0
  *   k_out, v_out out [tokens, heads, dim], 16-byte aligned, strides (in
@@ -691,7 +695,7 @@ pq_status pq_kv_load(const pq_kv_cache *cache, int dtype, int64_t batch, int64_t
  *   q, out       [batch, q_heads, dim] of q_dtype (PQ_BF16 or PQ_F16; the
  *                cache's dtype if that is PQ_KV_16), 16-byte aligned, strides
  *                (elements) multiples of 8
- *   q_heads      a positive multiple of cache->heads
+ *   q_heads      a positive multiple of cache->heads, at most 65535
  *   block_table  in [batch, max_pages] int32 with rows table_stride apart.
  *                Only the entries of attended tokens are used; a page id
  *                outside the cache hides its tokens

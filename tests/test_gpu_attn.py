@@ -394,3 +394,23 @@ def test_large_caches_are_streamed(pq, fmt, dim, group):
     out, lse = c.run(pq)
     c.check(out, lse)
     c.check(*want)
+
+
+def test_more_rows_than_one_launch_takes(pq):
+    """300 sequences of 65520 heads: 19.7 million rows, of which a launch takes 16.8."""
+    b, h, d, page = 300, 65520, 16, 16
+    cache = pq.KVCache.allocate(pq.PQ_KV_8, 1, page, h, d)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn(3, h, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    pq.pq_kv_append(cache, k, v, torch.arange(3, device=DEV))
+    q = torch.randn(b, h, d, generator=g, device=DEV).to(torch.bfloat16)
+    table, lens = torch.zeros(b, 1, dtype=torch.int32, device=DEV), torch.arange(b, device=DEV).to(torch.int32) % 4
+    out = torch.full_like(q, 7.0)
+    ws = pq.attn_workspace(cache, b, h)
+    pq.pq_attn_decode(cache, q, table, lens, out, workspace=ws)
+    part = torch.full_like(q[:100], 7.0)
+    for b0 in (0, 100, 200):
+        at = slice(b0, b0 + 100)
+        pq.pq_attn_decode(cache, q[at], table[at], lens[at], part, workspace=ws)
+        assert torch.equal(out[at], part)
+    assert torch.count_nonzero(out[::4]) == 0 and bool((out[1::4] != 0).any())

@@ -181,3 +181,21 @@ def test_launch_failure_reports_pq_err_hip(pq):
     assert pq.lib.pq_attn_decode(*attn_args(pq, c)) == 6
     assert pq.lib.pq_rope(pq.PQ_BF16, 3, 2, 64, 64, 0, 0, A, 128, 64, A, A, 100, B, 128, 64, None) == 6
     assert pq.lib.pq_rope_table(10, 64, 1e4, None, A, None) == 6
+
+
+def test_sizes_past_a_launch_are_refused(pq):
+    """A grid's threads are counted in 32 bits, and the rotation's heads too."""
+    rope = [pq.PQ_BF16, 3, 2, 64, 64, 0, 0, A, 128, 64, A, A, 100, B, 128, 64, None]
+    for at, value in ((1, 2 ** 26 - 3), (1, 2 ** 40), (2, 2 ** 31 - 1), (2, 2 ** 30 + 1), (2, 2 ** 40)):
+        a = list(rope)
+        a[at] = value
+        assert pq.lib.pq_rope(*a) == 2, (at, value)
+    c = cache(pq)
+    a = append_args(pq, c)
+    a[2] = 2 ** 26 - 3
+    assert pq.lib.pq_kv_append(*a) == 2
+    a = load_args(pq, c)
+    a[3] = 2 ** 28 - 15
+    assert pq.lib.pq_kv_load(*a) == 2
+    assert pq.lib.pq_rope_table(2 ** 27, 64, 1e4, None, A, None) == 2
+    assert pq.pq_attn_decode_workspace_bytes(type("C", (), {"ptr": ctypes.addressof(c)}), 1, 65536) == -1
