@@ -68,7 +68,9 @@ typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxBatch = 1024;     // sequences of one launch (their step counts sit in LDS)
-constexpr int kMaxShares = 512;     // blocks of one launch: two per CU
+// Blocks of one launch: two per CU.  (Of over 128 channels in 16 or 8 bits the
+// registers let a CU take one; it then takes its two one after the other.)
+constexpr int kMaxShares = 512;
 constexpr int kWaves = 4;
 // What a row costs a share beyond its steps (first loads, joining the waves,
 // a last round with idle waves), in steps of one wave.  64 ragged contexts of
@@ -800,9 +802,9 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         st.set_q(a);
         st.clear();
         int held_after = -1;
-        // Two blocks share a CU, and its older waves go first: a priority that
-        // falls with each quarter of the share keeps the two level (3 % of 64
-        // ragged 4-bit contexts).
+        // Two blocks share a CU (with the exception at kMaxShares), and its
+        // older waves go first: a priority that falls with each quarter of the
+        // share keeps the two level (3 % of 64 ragged 4-bit contexts).
         const int quarter = (end - begin + 3) >> 2;
         for (int i = 0; i < w.count; ++i) {
             const int done = w.row0 + kRowCost + w.step0 + i * kWaves - begin;

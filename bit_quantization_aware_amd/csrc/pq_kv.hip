@@ -32,10 +32,6 @@ struct RowLanes {
 
 // ------------------------------------------------------------------ append
 
-// Row groups a wave has in flight: one, and seven waves per SIMD (14 Ki tokens
-// of 30 heads of 80 channels, rows not yet packed: 38 us; two groups 40, four 47).
-constexpr int kAppendRows = 1;
-
 struct AppendArgs {
     uint8_t *k, *v;
     uint32_t *kp, *vp;
@@ -227,9 +223,11 @@ __device__ __forceinline__ u32x2 pack_codes(const float (&n)[8])
 // One wave per token and slice of its rows.  dim / 8 lanes hold a row, 8
 // channels each, and a wave takes a group of as many heads of K, V or Q as fit
 // at once (rows of 80 channels in 16 lanes each, with a butterfly in them,
-// waste six: 14 Ki tokens of 30 heads 38 us against 30); what kind of rows a group holds is the same
-// for the whole wave.  kAppendRows groups are
-// in flight, and the rotation's table values stay in registers over them.
+// waste six: 14 Ki tokens of 30 heads 38 us against 30); what kind of rows a
+// group holds is the same for the whole wave.  One group is in flight a wave (two
+// change little: 30 heads of 80 channels 30.0 us against 29.5, 48 of 128 70.2
+// against 72.3), and the rotation's table values stay in registers over all of
+// them.
 // What bounds it is vector instructions (some 600 a token at 30 heads of 80
 // channels), then the bytes.
 template <typename T, int FMT, typename CT>
@@ -259,67 +257,52 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     const int partner = d0 < a.rot / 2 ? d0 + a.rot / 2 : d0 - a.rot / 2;
 
     const int kv_groups = a.kv_groups;
-    for (int g0 = slice; g0 < a.groups; g0 += kAppendRows * a.slices) {
-        int kind[kAppendRows], head[kAppendRows];
-        bool live[kAppendRows];
-        const T *src[kAppendRows];
-        Raw8<T> own[kAppendRows], other[kAppendRows];
-#pragma unroll
-        for (int b = 0; b < kAppendRows; ++b) {
-            const int g = min(g0 + b * a.slices, a.groups - 1);
-            kind[b] = g < kv_groups ? 0 : g < 2 * kv_groups ? 1 : 2;
-            const int limit = kind[b] == 2 ? a.q_heads : a.heads;
-            const int h = (g - kind[b] * kv_groups) * a.lanes.side + sub;
-            live[b] = mine && h < limit;
-            head[b] = min(h, limit - 1);
-            src[b] = (kind[b] == 0 ? xk : kind[b] == 1 ? xv : xq) +
-                     head[b] * (kind[b] == 0 ? a.k_hs : kind[b] == 1 ? a.v_hs : a.q_hs);
-            own[b] = load_raw(src[b] + d0);
-            other[b] = own[b];
-            if (fetch && kind[b] != 1) other[b] = load_raw(src[b] + partner);
+    for (int g = slice; g < a.groups; g += a.slices) {
+        const int kind = g < kv_groups ? 0 : g < 2 * kv_groups ? 1 : 2;
+        const int limit = kind == 2 ? a.q_heads : a.heads;
+        const int h = (g - kind * kv_groups) * a.lanes.side + sub, head = min(h, limit - 1);
+        const bool live = mine && h < limit;
+        const T *src = (kind == 0 ? xk : kind == 1 ? xv : xq) + head * (kind == 0 ? a.k_hs : kind == 1 ? a.v_hs : a.q_hs);
+        const Raw8<T> own = load_raw(src + d0);
+        Raw8<T> other = own;
+        if (fetch && kind != 1) other = load_raw(src + partner);
+        float x[8];
+        raw_to_f32<T>(own, x);
+        if (kind != 1) apply_turn<T>(a, turn, other, src, d0, x);
+        if (kind == 2) {
+            // q_out may be q: a row is read and written by lanes of one wave,
+            // which has all it needs of it by now
+            if (live) store_f32<T, 8>(qo + head * a.qo_hs + d0, x);
+            continue;
         }
+        uint8_t *dst = (kind ? a.v : a.k) + in_page + head * a.head_stride;
+        if constexpr (FMT == PQ_KV_16) {
+            u32x4 w;
 #pragma unroll
-        for (int b = 0; b < kAppendRows; ++b) {
-            if (g0 + b * a.slices >= a.groups) break;
-            float x[8];
-            raw_to_f32<T>(own[b], x);
-            if (kind[b] != 1) apply_turn<T>(a, turn, other[b], src[b], d0, x);
-            if (kind[b] == 2) {
-                // q_out may be q: a row is read and written by lanes of one
-                // wave, which has all it needs of it by now
-                if (live[b]) store_f32<T, 8>(qo + head[b] * a.qo_hs + d0, x);
-                continue;
+            for (int e = 0; e < 4; ++e) w[e] = pack16<CT>(x[2 * e], x[2 * e + 1]);
+            if (live && stored) *reinterpret_cast<u32x4_a8 *>(dst + 2 * d0) = w;
+        } else {
+            constexpr float top = FMT == PQ_KV_8 ? 255.f : 15.f;
+            float mn = x[0], mx = x[0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) {
+                mn = min_nan(mn, x[e]);
+                mx = max_nan(mx, x[e]);
             }
-            uint8_t *dst = (kind[b] ? a.v : a.k) + in_page + head[b] * a.head_stride;
-            if constexpr (FMT == PQ_KV_16) {
-                u32x4 w;
+            row_range(a.lanes.n, ring, mn, mx);
+            const uint32_t sb = pack_bf16x2((mx - mn) * (1.f / top), mn);
+            const float s = fmaxf(bf16_to_f32(sb & 0xFFFFu), kMinKvScale), z = bf16_to_f32(sb >> 16);
+            const float inv = 1.f / s;
+            float n[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack16<CT>(x[2 * e], x[2 * e + 1]);
-                if (live[b] && stored) *reinterpret_cast<u32x4_a8 *>(dst + 2 * d0) = w;
-            } else {
-                constexpr float top = FMT == PQ_KV_8 ? 255.f : 15.f;
-                float mn = x[0], mx = x[0];
-#pragma unroll
-                for (int e = 1; e < 8; ++e) {
-                    mn = min_nan(mn, x[e]);
-                    mx = max_nan(mx, x[e]);
-                }
-                row_range(a.lanes.n, ring, mn, mx);
-                const uint32_t sb = pack_bf16x2((mx - mn) * (1.f / top), mn);
-                const float s = fmaxf(bf16_to_f32(sb & 0xFFFFu), kMinKvScale), z = bf16_to_f32(sb >> 16);
-                const float inv = 1.f / s;
-                float n[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    n[e] = __builtin_rintf(__builtin_amdgcn_fmed3f((x[e] - z) * inv, 0.f, top));
-                const u32x2 w = pack_codes<FMT>(n);
-                if (live[b] && stored) {
-                    if constexpr (FMT == PQ_KV_8) *reinterpret_cast<u32x2 *>(dst + d0) = w;
-                    else *reinterpret_cast<uint32_t *>(dst + d0 / 2) = w[0];
-                    if (d0 == 0)
-                        (kind[b] ? a.vp : a.kp)[((page * a.heads + head[b]) << a.page_log2) + off] =
-                            (__builtin_bit_cast(uint32_t, s) >> 16) | (sb & 0xFFFF0000u);
-                }
+            for (int e = 0; e < 8; ++e) n[e] = __builtin_rintf(__builtin_amdgcn_fmed3f((x[e] - z) * inv, 0.f, top));
+            const u32x2 w = pack_codes<FMT>(n);
+            if (live && stored) {
+                if constexpr (FMT == PQ_KV_8) *reinterpret_cast<u32x2 *>(dst + d0) = w;
+                else *reinterpret_cast<uint32_t *>(dst + d0 / 2) = w[0];
+                if (d0 == 0)
+                    (kind ? a.vp : a.kp)[((page * a.heads + head) << a.page_log2) + off] =
+                        (__builtin_bit_cast(uint32_t, s) >> 16) | (sb & 0xFFFF0000u);
             }
         }
     }

@@ -10,11 +10,9 @@
 
 namespace pq {
 
-// Accesses whose address is a multiple of 8 bytes only (4-bit rows, caller
-// strides): the hardware needs dword alignment.
+// Accesses whose address is a multiple of 8 bytes only (caller's strides): the
+// hardware needs dword alignment.
 typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
-typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
-typedef unsigned int u32_a2 __attribute__((aligned(2)));
 
 struct bf16_t { uint16_t bits; };
 struct f16_t { uint16_t bits; };
