@@ -74,7 +74,7 @@ constexpr int kMaxShares = 512;
 constexpr int kWaves = 4;
 // What a row costs a share beyond its steps (first loads, joining the waves,
 // a last round with idle waves), in steps of one wave.  64 ragged contexts of
-// 80 channels in 4 bits take 36.4 us with 8, 38.4 with 4, 36.8 with 12.
+// 80 channels in 4 bits take 37.6 us with 8, 39.3 with 4, 38.0 with 12.
 constexpr int kRowCost = 8;
 
 struct AttnArgs {
@@ -804,7 +804,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 1 : 2) void k_attn_decode(AttnArgs
         int held_after = -1;
         // Two blocks share a CU (with the exception at kMaxShares), and its
         // older waves go first: a priority that falls with each quarter of the
-        // share keeps the two level (3 % of 64 ragged 4-bit contexts).
+        // share keeps the two level (4 % of 64 ragged 4-bit contexts).
         const int quarter = (end - begin + 3) >> 2;
         for (int i = 0; i < w.count; ++i) {
             const int done = w.row0 + kRowCost + w.step0 + i * kWaves - begin;
@@ -989,19 +989,19 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a)
 
 // Rows of at most kWholeRow tokens are not split: one block takes such a row
 // in a few rounds, and a second launch would cost more (one bf16 sequence of
-// 1000 tokens 9.8 us against 11.4, of 2000 16.4 against 11.3; 64 of up to
-// 1000 in 8 bits, 512 rows, 21 against 29).  Where the rows alone fill the
-// chip that holds up to kWholeRowMany (512 rows of up to 2000 tokens 41 us
-// against 44; 128 rows 26 against 22).
+// 1000 tokens 9.8 us against 11.7, of 2000 16.1 against 11.6; 64 of up to
+// 1000 in 8 bits, 512 rows, 20 against 28).  Where the rows alone fill the
+// chip that holds up to kWholeRowMany (512 rows of evenly spread lengths up to
+// 2000 tokens 40 us against 41; 128 rows 26 against 22).
 constexpr int kWholeRow = 1024, kWholeRowMany = 2048;
 constexpr int kManyRows = 256;      // one per CU
 
 // A call whose cache is larger than the memory-side cache (256 MB) finds
 // nothing of it there: its loads are non-temporal then (32 contexts of 16 Ki
-// bf16 tokens, 1.9 GB: 293 us against 326), but only where a row is whole
+// bf16 tokens, 1.9 GB: 294 us against 315), but only where a row is whole
 // 128-byte lines, else lines that two loads share are fetched twice (bf16 rows
 // of 80 channels: 108 us against 85).  A smaller cache may still lie there
-// from the call before (16 chats, 67 MB: 21 us against 17.5).
+// from the call before (16 chats, 67 MB: 21 us against 17.2).
 constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 template <typename QT, int FMT, int DP, int R, bool NT>
@@ -1036,10 +1036,10 @@ template <typename QT, int FMT, int DP>
 void launch_copies(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
     // Two copies of the heads in the columns where the group leaves room, for
-    // 4 bits (64 ragged contexts of 64 channels 31 us against 36, of 128
-    // channels 43.7 against 45) of up to 128 channels (of 256: 65 against 53).
-    // More bytes a token outlast the softmax (8 bits, 128 channels: 72 us with
-    // two copies, 68 with one).
+    // 4 bits (64 ragged contexts of 64 channels 32 us against 38, of 128
+    // channels 43.9 against 45.8) of up to 128 channels (of 256: 66 against 53).
+    // More bytes a token outlast the softmax (8 bits, 128 channels: 71.5 us
+    // with two copies, 68.6 with one).
     if constexpr (FMT == PQ_KV_4 && DP <= 128) {
         if (a.group <= 8) return launch_stream<QT, FMT, DP, 2>(a, longest, s);
     }
@@ -1051,8 +1051,8 @@ void launch_dim(const AttnArgs &a, int64_t longest, hipStream_t s)
 {
     if (a.dim <= 64) return launch_copies<QT, FMT, 64>(a, longest, s);
     // Vector instructions bound 4 bits: the first product leaves out the last
-    // 32 channels where it can (64 contexts of 80 channels 35.2 us against
-    // 37.1).  Other formats wait for their bytes.
+    // 32 channels where it can (64 contexts of 80 channels 37.6 us against
+    // 38.5).  Other formats wait for their bytes.
     if constexpr (FMT == PQ_KV_4) {
         if (a.dim <= 96) return launch_copies<QT, FMT, 96>(a, longest, s);
     }

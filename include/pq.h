@@ -526,7 +526,8 @@ pq_status pq_weight_movement(int64_t rows, int64_t cols, const float *W, const f
  * packed-weight GEMMs.  The conventions at the top of this file hold, with
  * these additions: activations may be strided (strides in elements, the last
  * dimension contiguous); a NULL stream is the null stream; sizes of zero
- * enqueue nothing.
+ * enqueue nothing; a NaN that is copied stays one, but a signalling one of a
+ * 16-bit type becomes quiet.
  */
 
 /* Element types of activations (PQ_G_F32 and PQ_G_BF16 have the same values). */
