@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpq.so")
 SOURCES = ["pq_quant.hip", "pq_gemm.hip", "pq_gemm_big.hip", "pq_gemm_wres.hip", "pq_stats.hip", "pq_noalloc.hip",
-           "pq_rope.hip", "pq_kv.hip", "pq_attn.hip"]
+           "pq_rope.hip", "pq_kv.hip", "pq_attn.hip", "pq_norm.hip", "pq_gemm_a8.hip", "pq_distill.hip"]
 # the quantizer's kernels, one translation unit per mode (PQ_W1_BINARY .. PQ_W158_LSQ)
 MODE_SOURCE = "pq_quant_mode.hip"
 NUM_MODES = 7

@@ -38,7 +38,9 @@ EXPORTS = ("pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_
            "pq_qat_step_grouped", "pq_pack", "pq_gemm", "pq_gemm_f32a", "pq_num_levels", "pq_level_stats",
            "pq_quantize_fwd_stats", "pq_weight_movement", "pq_pack_grouped", "pq_gemm_noalloc",
            "pq_rope_table", "pq_rope", "pq_kv_row_bytes", "pq_kv_append", "pq_kv_load",
-           "pq_attn_decode_workspace_bytes", "pq_attn_decode")
+           "pq_attn_decode_workspace_bytes", "pq_attn_decode",
+           "pq_rmsnorm", "pq_rmsnorm_bwd_workspace_bytes", "pq_rmsnorm_bwd", "pq_quantize_rows",
+           "pq_gemm_a8_workspace_bytes", "pq_gemm_a8", "pq_distill", "pq_distill_bwd")
 
 
 class PQError(RuntimeError):
@@ -84,6 +86,13 @@ class pq_kv_cache(ctypes.Structure):
                 ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("format", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class pq_epilogue(ctypes.Structure):
+    """Mirror of `struct pq_epilogue` in include/pq.h."""
+    _fields_ = [("bias", ctypes.c_void_p), ("other", ctypes.c_void_p), ("other_stride", ctypes.c_int64),
+                ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("combine", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 def _load():
@@ -134,8 +143,19 @@ def _load():
     L.pq_attn_decode_workspace_bytes.restype = i64
     L.pq_attn_decode.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, i64, i64, vp, dbl, i64, i64, vp, i64, i64,
                                  vp, vp, i64, vp]
+    L.pq_rmsnorm.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, i32, dbl, vp, i64, vp, i64, vp, vp, vp]
+    L.pq_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i64]
+    L.pq_rmsnorm_bwd_workspace_bytes.restype = i64
+    L.pq_rmsnorm_bwd.argtypes = [i32, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp]
+    L.pq_quantize_rows.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp]
+    L.pq_gemm_a8_workspace_bytes.argtypes = [i32, i64, i64, i64]
+    L.pq_gemm_a8_workspace_bytes.restype = i64
+    L.pq_gemm_a8.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, vp, i32, vp, i32, vp, i64, vp, i64, vp]
+    L.pq_distill.argtypes = [i32, i64, i64, vp, i64, i64, vp, vp, i32, dbl, vp, vp, vp, dbl, vp, i64, vp]
+    L.pq_distill_bwd.argtypes = [i32, i64, i64, vp, i64, i64, vp, vp, i32, dbl, vp, vp, vp, vp, i64, vp]
     for name in EXPORTS:
-        if name not in ("pq_kv_row_bytes", "pq_attn_decode_workspace_bytes", "pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_status_str",
+        if name not in ("pq_rmsnorm_bwd_workspace_bytes", "pq_gemm_a8_workspace_bytes",
+                        "pq_kv_row_bytes", "pq_attn_decode_workspace_bytes", "pq_code_row_bytes", "pq_packed_bytes", "pq_default_grad_scale", "pq_status_str",
                         "pq_version", "pq_num_levels", "pq_gemm_workspace_bytes"):
             getattr(L, name).restype = i32
     return L
@@ -614,3 +634,202 @@ def pq_attn_decode(cache: KVCache, q, block_table, lens, out, lse=None, scale=No
                             workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     if rc:
         raise PQError(rc, "pq_attn_decode")
+
+
+# ------------------------------------------------- around the packed product
+# Normalisation, rows in 8 bits, the product of 8-bit activations with its
+# epilogue, and distillation.  Matrices are 2-dimensional tensors with a
+# contiguous last dimension.
+
+PQ_ACT_NONE, PQ_ACT_RELU, PQ_ACT_SILU, PQ_ACT_GELU, PQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
+PQ_COMBINE_ADD, PQ_COMBINE_MUL = 0, 1
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The current device, which all of a call's tensors have to be on."""
+    d = t.get_device()
+    if d != torch.cuda.current_device():
+        raise ValueError(f"{what}: a tensor on the current GPU wanted")
+    return d
+
+
+def _matrix(t: torch.Tensor, shape, dtype, what: str, device: int):
+    """(address, row stride in elements) of t [rows, cols] of a type."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{what}: {dtype} {list(shape)} on the call's device wanted")
+    st = t.stride()
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: a contiguous last dimension wanted")
+    return t.data_ptr(), st[0]
+
+
+def _matrix_shape(t: torch.Tensor, what: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: [rows, cols] wanted")
+    return shape
+
+
+def _vector(t: torch.Tensor, dtype, n: int, what: str, device: int) -> int:
+    """The address of a contiguous array of n elements."""
+    if t.dtype != dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous {dtype} on the call's device wanted")
+    return t.data_ptr()
+
+
+def _optional(t, dtype, n, what, device):
+    return None if t is None else _vector(t, dtype, n, what, device)
+
+
+def _buffer(t, device: int):
+    """(address, bytes) of a workspace, or of none."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on the call's device wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def pq_rmsnorm(x, weight, y=None, residual=None, sum=None, q=None, scale=None, rstd=None, eps=1e-6, stream=None) -> None:
+    """Norm of x (+ residual, stored in sum) [rows, cols] into y, or into int8 rows q with their scales."""
+    rows, cols = shape = _matrix_shape(x, "x")
+    kind, dev = x.dtype, _device(x, "x")
+    xp, xs = _matrix(x, shape, kind, "x", dev)
+    rp = sp = yp = qp = cp = None
+    rs = ss = ys = qs = 0
+    if residual is not None:
+        rp, rs = _matrix(residual, shape, kind, "residual", dev)
+    if sum is not None:
+        sp, ss = _matrix(sum, shape, kind, "sum", dev)
+    if y is not None:
+        yp, ys = _matrix(y, shape, kind, "y", dev)
+    if q is not None:
+        qp, qs = _matrix(q, shape, torch.int8, "q", dev)
+        cp = _optional(scale, torch.float32, rows, "scale", dev)
+    rc = lib.pq_rmsnorm(_dtype(x, "x"), rows, cols, xp, xs, rp, rs, sp, ss, _vector(weight, weight.dtype, cols, "weight", dev),
+                        _dtype(weight, "weight"), eps, yp, ys, qp, qs, cp,
+                        _optional(rstd, torch.float32, rows, "rstd", dev), _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_rmsnorm")
+
+
+def pq_rmsnorm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib.pq_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def rmsnorm_bwd_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """A workspace for pq_rmsnorm_bwd calls of this size, for the caller to keep."""
+    n = pq_rmsnorm_bwd_workspace_bytes(rows, cols)
+    if n < 0:
+        raise PQError(2, "pq_rmsnorm_bwd_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def pq_rmsnorm_bwd(h, weight, rstd, dy, dx, dsum=None, dweight=None, workspace=None, stream=None) -> None:
+    """Gradient of pq_rmsnorm from what it normalised (h) and its rstd; dsum is the gradient that reaches h from
+    elsewhere.  Without a workspace one is allocated for dweight."""
+    rows, cols = shape = _matrix_shape(h, "h")
+    kind, dev = h.dtype, _device(h, "h")
+    hp, hs = _matrix(h, shape, kind, "h", dev)
+    yp, ys = _matrix(dy, shape, kind, "dy", dev)
+    xp, xs = _matrix(dx, shape, kind, "dx", dev)
+    sp, ss = (None, 0) if dsum is None else _matrix(dsum, shape, kind, "dsum", dev)
+    if dweight is not None and workspace is None:
+        with _memory_of(stream):
+            workspace = rmsnorm_bwd_workspace(rows, cols, h.device)
+    rc = lib.pq_rmsnorm_bwd(_dtype(h, "h"), rows, cols, hp, hs, _vector(weight, weight.dtype, cols, "weight", dev),
+                            _dtype(weight, "weight"), _vector(rstd, torch.float32, rows, "rstd", dev), yp, ys, sp, ss, xp, xs,
+                            _optional(dweight, torch.float32, cols, "dweight", dev), *_buffer(workspace, dev),
+                            _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_rmsnorm_bwd")
+
+
+def pq_quantize_rows(x, q, scale, stream=None) -> None:
+    """x [rows, cols] as int8 rows q with their scales."""
+    rows, cols = shape = _matrix_shape(x, "x")
+    dev = _device(x, "x")
+    xp, xs = _matrix(x, shape, x.dtype, "x", dev)
+    qp, qs = _matrix(q, shape, torch.int8, "q", dev)
+    rc = lib.pq_quantize_rows(_dtype(x, "x"), rows, cols, xp, xs, qp, qs,
+                              _vector(scale, torch.float32, rows, "scale", dev), _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_quantize_rows")
+
+
+def pq_gemm_a8_workspace_bytes(mode: int, M: int, N: int, K: int) -> int:
+    return int(lib.pq_gemm_a8_workspace_bytes(mode, M, N, K))
+
+
+def a8_workspace(mode: int, M: int, N: int, K: int, device="cuda") -> Optional[torch.Tensor]:
+    """A workspace for pq_gemm_a8 calls of this shape (None when it needs none), for the caller to keep."""
+    n = pq_gemm_a8_workspace_bytes(mode, M, N, K)
+    if n < 0:
+        raise PQError(2, "pq_gemm_a8_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def pq_gemm_a8(mode, x, x_scale, packed, alpha, y, bias=None, activation=PQ_ACT_NONE, other=None, combine=PQ_COMBINE_ADD,
+               workspace=None, stream=None) -> None:
+    """y [M, N] = act(x_scale alpha (x @ levels^T) + bias) (+ or *) other, of int8 rows x [M, K] and packed weights."""
+    M, K = xshape = _matrix_shape(x, "x")
+    N = y.shape[1] if y.dim() == 2 else -1
+    kind, dev = y.dtype, _device(x, "x")
+    xp, xs = _matrix(x, xshape, torch.int8, "x", dev)
+    yp, ys = _matrix(y, (M, N), kind, "y", dev)
+    e = pq_epilogue(None, None, 0, 0, activation, combine, 0)
+    if bias is not None:
+        e.bias, e.bias_dtype = _vector(bias, bias.dtype, N, "bias", dev), _dtype(bias, "bias")
+    if other is not None:
+        e.other, e.other_stride = _matrix(other, (M, N), kind, "other", dev)
+    if M == 1 and xs < K:                # the stride of a single row does not matter
+        xs = K
+    if packed.dtype != torch.uint8 or packed.numel() < pq_packed_bytes(mode, N, K) or packed.get_device() != dev or \
+            not packed.is_contiguous():
+        raise ValueError("packed: the uint8 array of pq_pack on the call's device wanted")
+    if workspace is None:
+        with _memory_of(stream):
+            workspace = a8_workspace(mode, M, N, K, x.device)
+    rc = lib.pq_gemm_a8(mode, M, N, K, xp, xs, _vector(x_scale, torch.float32, M, "x_scale", dev), packed.data_ptr(),
+                        _vector(alpha, alpha.dtype, N, "alpha", dev), _dtype(alpha, "alpha"), ctypes.addressof(e),
+                        _dtype(y, "y"), yp, ys, *_buffer(workspace, dev), _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_gemm_a8")
+
+
+def _teacher(logits, index, top):
+    rows, vocab = shape = _matrix_shape(logits, "logits")
+    dev = _device(logits, "logits")
+    n = index.shape
+    if len(n) != 2 or n[0] != rows or top.shape != n:
+        raise ValueError("index, top: [rows, k] wanted")
+    return rows, vocab, shape, dev, n[1], _vector(index, torch.int32, rows * n[1], "index", dev), \
+        _vector(top, top.dtype, rows * n[1], "top", dev), _dtype(top, "top")
+
+
+def pq_distill(logits, index, top, loss=None, stats=None, dlogits=None, temperature=1.0, row_weight=None, grad_scale=1.0,
+               stream=None) -> None:
+    """Loss of logits [rows, vocab] against a teacher's top logits at index [rows, k], with what pq_distill_bwd takes
+    (stats [rows, 2]) and the gradient of grad_scale * loss.sum() on request."""
+    rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
+    lp, ls = _matrix(logits, shape, logits.dtype, "logits", dev)
+    dp, ds = (None, 0) if dlogits is None else _matrix(dlogits, shape, logits.dtype, "dlogits", dev)
+    rc = lib.pq_distill(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
+                        _optional(row_weight, torch.float32, rows, "row_weight", dev),
+                        _optional(loss, torch.float32, rows, "loss", dev), _optional(stats, torch.float32, 2 * rows, "stats", dev),
+                        grad_scale, dp, ds, _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_distill")
+
+
+def pq_distill_bwd(logits, index, top, stats, dloss, dlogits, temperature=1.0, row_weight=None, stream=None) -> None:
+    """Gradient of pq_distill's loss, weighed by dloss [rows], into dlogits (which may be logits)."""
+    rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
+    lp, ls = _matrix(logits, shape, logits.dtype, "logits", dev)
+    dp, ds = _matrix(dlogits, shape, logits.dtype, "dlogits", dev)
+    rc = lib.pq_distill_bwd(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
+                            _optional(row_weight, torch.float32, rows, "row_weight", dev),
+                            _vector(stats, torch.float32, 2 * rows, "stats", dev), _vector(dloss, torch.float32, rows, "dloss", dev),
+                            dp, ds, _stream(stream))
+    if rc:
+        raise PQError(rc, "pq_distill_bwd")

@@ -724,6 +724,154 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
                          int64_t max_len, void *out, int64_t out_batch_stride, int64_t out_head_stride, float *lse,
                          void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * Around the packed product: normalisation, rows in 8 bits, the product of
+ * 8-bit activations with its epilogue, and distillation.  The conventions of
+ * the serving operators above hold (strides in elements, the last dimension
+ * contiguous, sizes of zero enqueue nothing); matrices need the alignment of
+ * their elements only, unless said otherwise, and scales, statistics and
+ * losses are fp32.  An output may be the same array as an input where that is
+ * said (same address, same stride); any other overlap is not allowed.  For
+ * fixed arguments every result is the same in every run.
+ *
+ * Rows in 8 bits: row m of a matrix y is held as int8 codes q in -127 .. 127
+ * and one fp32 scale, standing for y^ = scale[m] q:
+ *   scale = max(max_j |y_j| fl32(1/127), 2^-60),   q_j = rint(y_j / scale)
+ * in fp32 (the quotient as a product with the reciprocal), rint to even.  A
+ * row that holds a NaN or an infinity has a NaN scale, and so no values.
+ */
+
+/* pq_rmsnorm -- root-mean-square norm, with the residual's addition and an
+ * output in 8 bits on request:
+ *   h = x + residual (rounded to the type; x itself without a residual)
+ *   y = h rstd weight,   rstd = (mean_j h_j^2 + eps)^(-1/2)
+ * in fp32, y rounded once -- to the type, or to 8 bits as above.
+ *   dtype      of x, residual, sum and y: PQ_F32, PQ_BF16 or PQ_F16
+ *   rows       at most 2^31 - 1;  cols 1 .. 32768
+ *   residual   in [rows, cols], or NULL;  sum out h, required with it (NULL
+ *              without); sum may be x or residual
+ *   weight     in [cols] of w_dtype (as dtype)
+ *   eps        > 0
+ *   y          out [rows, cols], or NULL; may be x (then not also sum's)
+ *   q, scale   out [rows, cols] int8 and [rows]: the row in 8 bits, instead of
+ *              y (exactly one of y and q; else PQ_ERR_ARG)
+ *   rstd       out [rows], or NULL: what pq_rmsnorm_bwd takes */
+pq_status pq_rmsnorm(int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride, const void *residual,
+                     int64_t r_stride, void *sum, int64_t s_stride, const void *weight, int w_dtype, double eps,
+                     void *y, int64_t y_stride, int8_t *q, int64_t q_stride, float *scale, float *rstd, void *stream);
+
+/* pq_rmsnorm_bwd -- its gradient, from h (x, or sum where there was a residual):
+ *   n = h rstd,   g = dy weight
+ *   dx = rstd (g - n mean_j(g_j n_j)) + dsum      (x's and the residual's alike)
+ *   dweight_j = sum over the rows of dy_j n_j
+ *   dtype      of h, dy, dsum and dx
+ *   dsum       in: the gradient that reaches h from elsewhere, or NULL
+ *   dx         out; may be dy or dsum
+ *   dweight    out [cols] fp32, or NULL
+ *   workspace  device memory of pq_rmsnorm_bwd_workspace_bytes(rows, cols)
+ *              bytes, 16-byte aligned, for dweight (NULL without it); its
+ *              contents on entry do not matter.  Calls that overlap need
+ *              different ones */
+int64_t pq_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+pq_status pq_rmsnorm_bwd(int dtype, int64_t rows, int64_t cols, const void *h, int64_t h_stride, const void *weight,
+                         int w_dtype, const float *rstd, const void *dy, int64_t dy_stride, const void *dsum,
+                         int64_t ds_stride, void *dx, int64_t dx_stride, float *dweight, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/* pq_quantize_rows -- x [rows, cols] (cols 1 .. 65536) in 8 bits as above. */
+pq_status pq_quantize_rows(int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride, int8_t *q,
+                           int64_t q_stride, float *scale, void *stream);
+
+/* Activations of the product's epilogue: none, max(v, 0), v / (1 + e^-v),
+ * v (1 + erf(v / sqrt 2)) / 2, and the latter's tanh form
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+#define PQ_ACT_NONE 0
+#define PQ_ACT_RELU 1
+#define PQ_ACT_SILU 2
+#define PQ_ACT_GELU 3
+#define PQ_ACT_GELU_TANH 4
+
+/* What the epilogue does with `other`: adds it (a residual) or multiplies by
+ * it (the other half of a gated layer). */
+#define PQ_COMBINE_ADD 0
+#define PQ_COMBINE_MUL 1
+
+typedef struct pq_epilogue {
+    const void *bias;     /* [N] of bias_dtype, or NULL                     */
+    const void *other;    /* [M, N] of y's dtype, or NULL                   */
+    int64_t other_stride; /* elements between its rows                      */
+    int32_t bias_dtype;   /* PQ_F32, PQ_BF16, PQ_F16                        */
+    int32_t activation;   /* PQ_ACT_..                                      */
+    int32_t combine;      /* PQ_COMBINE_.. (without `other`: not used)      */
+    int32_t reserved;     /* 0                                              */
+} pq_epilogue;
+
+/*
+ * pq_gemm_a8 -- the packed product on activations in 8 bits:
+ *   v[m, n] = x_scale[m] alpha[n] sum_k X[m, k] level(code[n, k]) + bias[n]
+ *   Y[m, n] = act(v) (+ or *) other[m, n]
+ * with pq_gemm's weights and levels.  The levels of every width are whole
+ * numbers times a power of two (ternary: times fl32(2/3)), so the sum over k
+ * is an integer sum on the matrix unit and exact; what follows is fp32,
+ * rounded once to y's type.
+ *   mode       a deployable width
+ *   M, N       0 .. 2^24;  K a positive multiple of 64, at most 2^17 - 64
+ *              (the sums then fit 32 bits)
+ *   X          in [M, K] int8 codes, 16-byte aligned, x_stride (at least K) a
+ *              multiple of 16
+ *   x_scale    in [M]
+ *   packed     in pq_packed_bytes(mode, N, K) bytes in the export byte order
+ *   alpha      in [N] of alpha_dtype: PQ_BF16 (the exported scale) or PQ_F32
+ *   epilogue   host pointer read during the call, or NULL for none
+ *   Y          out [M, N] of y_dtype: PQ_F32, PQ_BF16 or PQ_F16; may be
+ *              epilogue->other (with the same stride)
+ *   workspace  device memory of pq_gemm_a8_workspace_bytes(mode, M, N, K)
+ *              bytes, 16-byte aligned (NULL where that is 0); its contents on
+ *              entry do not matter.  Calls that overlap need different ones
+ */
+int64_t pq_gemm_a8_workspace_bytes(int mode, int64_t M, int64_t N, int64_t K);
+pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t x_stride,
+                     const float *x_scale, const uint8_t *packed, const void *alpha, int alpha_dtype,
+                     const pq_epilogue *epilogue, int y_dtype, void *Y, int64_t y_stride, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * pq_distill -- distillation from a teacher's top logits.  Row r's teacher
+ * gives logits top[r, j] at words index[r, j], j < k; with temperature T
+ *   p = softmax_j(top[r, j] / T) over the entries with an index in
+ *       [0, vocab) (others do not count; a word that is named twice has the
+ *       sum of both),   q = softmax_i(logits[r, i] / T) over all words
+ *   loss[r] = row_weight[r] T^2 sum_j p_j (ln p_j - ln q_index[j])
+ *   dlogits[r, i] = grad_scale row_weight[r] T (q_i - p_i)
+ * i.e. the gradient of grad_scale * sum_r loss[r], computed while the row is
+ * at hand.  A row of weight 0 or without a valid entry has loss 0 and gradient
+ * 0, whatever its logits hold; an entry of p_j = 0 adds nothing to the loss.
+ * A logit of -inf has q_i = 0; NaN, +inf and rows of nothing but -inf give NaN.
+ *   dtype       of logits and dlogits
+ *   rows        at most 2^31 - 1;  vocab 1 .. 2^30;  k 1 .. 1024
+ *   index       in [rows, k] int32, top in [rows, k] of top_dtype
+ *   temperature > 0
+ *   row_weight  in [rows], or NULL for 1
+ *   loss        out [rows], or NULL
+ *   stats       out [rows, 2]: (max_i logits_i, sum_i exp((logits_i - max) / T)),
+ *               what pq_distill_bwd takes, or NULL
+ *   dlogits     out [rows, vocab], or NULL; may be logits
+ * At least one of loss, stats and dlogits is wanted.  Sums are fp32, the loss
+ * of a row is put together in binary64 and rounded once.
+ */
+pq_status pq_distill(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t l_stride, int64_t k,
+                     const int32_t *index, const void *top, int top_dtype, double temperature,
+                     const float *row_weight, float *loss, float *stats, double grad_scale, void *dlogits,
+                     int64_t d_stride, void *stream);
+
+/* pq_distill_bwd -- the gradient by itself, for losses that are weighed later:
+ * dlogits[r, i] = dloss[r] row_weight[r] T (q_i - p_i), from the stats of
+ * pq_distill on the same logits.  dlogits may be logits. */
+pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t l_stride, int64_t k,
+                         const int32_t *index, const void *top, int top_dtype, double temperature,
+                         const float *row_weight, const float *stats, const float *dloss, void *dlogits,
+                         int64_t d_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
