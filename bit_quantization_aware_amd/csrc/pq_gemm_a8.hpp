@@ -7,7 +7,7 @@
 #include <stdint.h>
 
 #include "pq_gemm_common.hpp"
-#include "pq_kv_common.hpp"
+#include "pq_row_common.hpp"
 
 namespace pq {
 namespace {
@@ -84,67 +84,69 @@ __device__ __forceinline__ intx4 decode(const A8Args &a, const Words<1> &c)
     return r;
 }
 
-__device__ __forceinline__ float any_f32(const void *p, int dtype, int64_t i)
-{
-    if (dtype == PQ_F32) return static_cast<const float *>(p)[i];
-    if (dtype == PQ_BF16) return to_f32(static_cast<const bf16_t *>(p)[i]);
-    return to_f32(static_cast<const f16_t *>(p)[i]);
-}
-
-// e^-x by the hardware's exponential and a reciprocal: both are off by a unit
-// of the last place of fp32, as the products around them.
+// e^-x and 1 / x by the hardware's exponential and reciprocal, each within a
+// unit of fp32's last place.
 __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(-1.4426950408889634f * x); }
 
-__device__ __forceinline__ float activate(float v, int act)
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act)
 {
-    if (act == PQ_ACT_RELU) return v < 0.f ? 0.f : v;        // NaN stays
-    if (act == PQ_ACT_SILU) return v / (1.f + exp_neg(v));
-    if (act == PQ_ACT_GELU) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    if (act == PQ_ACT_GELU_TANH) {
-        // 1 + tanh(u) = 2 / (1 + e^-2u)
-        const float u = 0.7978845608028654f * (v + 0.044715f * v * v * v);
-        return v / (1.f + exp_neg(2.f * u));
-    }
-    return v;
-}
-
-// One output: row's scale times column's scale, bias, activation, other.
-__device__ __forceinline__ float finish(const A8Args &a, int sum, float row_scale, float col_scale, float bias, float other)
-{
-    const float v = activate(__builtin_fmaf(static_cast<float>(sum), row_scale * col_scale, bias), a.act);
-    return a.mul ? v * other : v + other;
-}
-
-// Four consecutive columns of a row, n0 .. n0 + 3 (those below N).
-__device__ __forceinline__ void store4(const A8Args &a, int m, int n0, const intx4 &sum, const float (&cs)[4], const float (&cb)[4])
-{
-    const float rs = a.x_scale[m];
-    float y[4];
+    if (act == PQ_ACT_RELU) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int n = min(n0 + e, a.N - 1);
-        const float other = a.other ? any_f32(a.other, a.y_dtype, m * a.o_st + n) : 0.f;
-        y[e] = finish(a, sum[e], rs, cs[e], cb[e], other);
-    }
+        for (int e = 0; e < N; ++e) v[e] = v[e] < 0.f ? 0.f : v[e];      // NaN stays
+    } else if (act == PQ_ACT_SILU) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (n0 + e >= a.N) break;
-        const int64_t at = m * a.y_st + n0 + e;
-        if (a.y_dtype == PQ_F32) static_cast<float *>(a.Y)[at] = y[e];
-        else if (a.y_dtype == PQ_BF16) static_cast<bf16_t *>(a.Y)[at] = from_f32<bf16_t>(y[e]);
-        else static_cast<f16_t *>(a.Y)[at] = from_f32<f16_t>(y[e]);
+        for (int e = 0; e < N; ++e) v[e] *= __builtin_amdgcn_rcpf(1.f + exp_neg(v[e]));
+    } else if (act == PQ_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = 0.5f * v[e] * (1.f + erff(v[e] * 0.70710678118654752f));
+    } else if (act == PQ_ACT_GELU_TANH) {
+        // (1 + tanh u) / 2 = 1 / (1 + e^-2u)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            v[e] *= __builtin_amdgcn_rcpf(1.f + exp_neg(1.5957691216057308f * v[e] * (1.f + 0.044715f * v[e] * v[e])));
     }
 }
 
-// Scale (with the levels' unit) and bias of columns n0 .. n0 + 3.
-__device__ __forceinline__ void columns4(const A8Args &a, int n0, float (&cs)[4], float (&cb)[4])
+// Scale (with the levels' unit) and bias of columns 8c .. 8c + 7 (0 past N).
+__device__ __forceinline__ void columns8(const A8Args &a, int c, float (&cs)[8], float (&cb)[8])
 {
+    load_any8(a.alpha, a.alpha_dtype, c, a.N, cs);
+    if (a.bias) {
+        load_any8(a.bias, a.bias_dtype, c, a.N, cb);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int n = min(n0 + e, a.N - 1);
-        cs[e] = any_f32(a.alpha, a.alpha_dtype, n) * a.unit;
-        cb[e] = a.bias ? any_f32(a.bias, a.bias_dtype, n) : 0.f;
+        for (int e = 0; e < 8; ++e) cb[e] = 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] *= a.unit;
+}
+
+// Eight outputs of row m, columns 8c .. 8c + 7: scales, bias, activation,
+// other, and the store.
+template <typename T>
+__device__ __forceinline__ void finish8(const A8Args &a, int64_t m, int c, float row_scale, const int (&sum)[8], const float (&cs)[8],
+                                        const float (&cb)[8])
+{
+    float v[8], o[8];
+    if (a.other) raw_to_f32<T>(load_row8(static_cast<const T *>(a.other) + m * a.o_st, c, a.N), o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(static_cast<float>(sum[e]), row_scale * cs[e], cb[e]);
+    activate(v, a.act);
+    if (a.other) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = a.mul ? v[e] * o[e] : v[e] + o[e];
+    }
+    store_row8<T>(static_cast<T *>(a.Y) + m * a.y_st, c, a.N, v);
+}
+
+// f(T{}) for y's type.
+template <typename F>
+__device__ __forceinline__ void with_type(int dtype, F &&f)
+{
+    if (dtype == PQ_F32) f(float{});
+    else if (dtype == PQ_BF16) f(bf16_t{});
+    else f(f16_t{});
 }
 
 }  // namespace

@@ -817,8 +817,8 @@ typedef struct pq_epilogue {
  *   mode       a deployable width
  *   M, N       0 .. 2^24;  K a positive multiple of 64, at most 2^17 - 64
  *              (the sums then fit 32 bits)
- *   X          in [M, K] int8 codes, 16-byte aligned, x_stride (at least K) a
- *              multiple of 16
+ *   X          in [M, K] int8 codes, 16-byte aligned, x_stride a multiple of 16,
+ *              K .. 2^23
  *   x_scale    in [M]
  *   packed     in pq_packed_bytes(mode, N, K) bytes in the export byte order
  *   alpha      in [N] of alpha_dtype: PQ_BF16 (the exported scale) or PQ_F32
