@@ -18,64 +18,78 @@ constexpr int64_t kMaxA8K = (int64_t(1) << 17) - 64;
 constexpr int64_t kMaxA8 = int64_t(1) << 24;
 constexpr int64_t kMaxXStride = int64_t(1) << 23;    // a tile's rows are within 32 bits of its first
 
-// One 16-column tile by 16 MT rows a block; its four waves take every fourth
-// 64-byte group of K and add their sums through LDS.  No activations in LDS:
-// a lane reads the sixteen values its codes stand against.
-template <int BITS, int MT>
-__global__ __launch_bounds__(256) void k_a8_stream(A8Args a)
+// Up to 16 rows: the weights' stream bounds it, so a block takes NT 16-column
+// tiles, its eight waves every eighth 64-byte group of K, and the code bytes go
+// to registers with the streaming hint (they are read once).  No activations
+// in LDS: a lane reads the sixteen values that its codes stand against.  The
+// loads of U groups, and what the epilogue reads, are in flight before the
+// first is used.
+template <int BITS, int NT, int U>
+__global__ __launch_bounds__(512) void k_a8_stream(A8Args a)
 {
-    __shared__ intx4 red[4][16 * MT * 5];       // rows of 16 sums, 16 bytes apart
+    constexpr int GK = 512 / BITS, STEPS = GK / 64;             // k and products of a group
+    __shared__ intx4 red[8][NT][16 * 5];        // a wave's sums: rows of 16, 16 bytes apart
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int i16 = lane & 15, g = lane >> 4;
-    const int tile = blockIdx.x, m0 = blockIdx.y * (16 * MT);
-    constexpr int GK = 512 / BITS;              // k of a 64-byte group
-    const int groups = (a.K + GK - 1) / GK;
-    intx4 acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = intx4{0, 0, 0, 0};
-    const int8_t *x[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) x[t] = a.X + min(m0 + 16 * t + i16, a.M - 1) * a.x_st;
-    for (int q = w; q < groups; q += 4) {
-        const u32x4 c = *reinterpret_cast<const u32x4 *>(a.packed + q * a.gstride + static_cast<int64_t>(tile) * 1024 +
-                                                          i16 * 64 + g * 16);
-#pragma unroll
-        for (int j = 0; j < GK / 64; ++j) {
-            Words<BITS> wd;
-            if constexpr (BITS == 1) wd.w = c[j >> 1] >> (16 * (j & 1));
-            if constexpr (BITS == 2) wd.w = c[j];
-            if constexpr (BITS == 4) wd = {c[2 * j], c[2 * j + 1]};
-            const intx4 b = decode(a, wd);
-            const int k = q * GK + g * (GK / 4) + j * 16;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                intx4 v = {0, 0, 0, 0};
-                if (k < a.K) v = *reinterpret_cast<const intx4 *>(x[t] + k);
-                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, v, acc[t], 0, 0, 0);
-            }
-        }
+    const int groups = (a.K + GK - 1) / GK, last_tile = (a.N - 1) >> 4;
+    // the epilogue's share of a lane: eight columns of a row, in the last waves
+    const int to = static_cast<int>(threadIdx.x) - (512 - 32 * NT), r = (to >> 1) & 15, tile = to >> 5, h = to & 1;
+    const int c = (blockIdx.x * NT + tile) * 2 + h;
+    const bool writes = to >= 0 && r < a.M && 8 * c < a.N;
+    float cs[8], cb[8], rs = 0.f;
+    if (writes) {
+        columns8(a, c, cs, cb);
+        rs = a.x_scale[r];
     }
-    // Sums of the four waves; a lane then takes eight columns of a row.
+    intx4 acc[NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[w][(16 * t + i16) * 5 + g] = acc[t];
-    __syncthreads();
-    const int c = tile * 2 + (threadIdx.x & 1);
-    if (8 * c >= a.N) return;
-    float cs[8], cb[8];
-    columns8(a, c, cs, cb);
-    with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) {
-        for (int r = threadIdx.x >> 1; r < min(16 * MT, a.M - m0); r += 128) {
-            int sum[8];
+    for (int t = 0; t < NT; ++t) acc[t] = intx4{0, 0, 0, 0};
+    const int8_t *x = a.X + min(i16, a.M - 1) * a.x_st;
+    const uint8_t *codes[NT];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int at = r * 5 + 2 * (threadIdx.x & 1) + h;
-                const intx4 v = red[0][at] + red[1][at] + red[2][at] + red[3][at];
+    for (int t = 0; t < NT; ++t)
+        codes[t] = a.packed + static_cast<int64_t>(min(static_cast<int>(blockIdx.x) * NT + t, last_tile)) * 1024 + i16 * 64 + g * 16;
+    for (int q0 = w; q0 < groups; q0 += 8 * U) {
+        u32x4 cw[U][NT];
+        intx4 v[U][STEPS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[4 * h + e] = v[e];
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                cw[u][t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes[t] + min(q0 + 8 * u, groups - 1) * a.gstride));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) {
+                const int k = (q0 + 8 * u) * GK + g * (GK / 4) + j * 16;      // past K: no product
+                v[u][j] = intx4{0, 0, 0, 0};
+                if (k < a.K) v[u][j] = *reinterpret_cast<const intx4 *>(x + k);
             }
-            finish8<decltype(type)>(a, m0 + r, c, a.x_scale[m0 + r], sum, cs, cb);
-        }
-    });
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    Words<BITS> wd;
+                    if constexpr (BITS == 1) wd.w = cw[u][t][j >> 1] >> (16 * (j & 1));
+                    if constexpr (BITS == 2) wd.w = cw[u][t][j];
+                    if constexpr (BITS == 4) wd = {cw[u][t][2 * j], cw[u][t][2 * j + 1]};
+                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode(a, wd), v[u][j], acc[t], 0, 0, 0);
+                }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) red[w][t][i16 * 5 + g] = acc[t];
+    __syncthreads();
+    if (!writes) return;
+    int sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += red[i][tile][r * 5 + 2 * h + (e >> 2)][e & 3];
+    with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, r, c, rs, sum, cs, cb); });
 }
 
 // Output tiles of many rows: WN waves side by side, each 16 MT rows by 16 NT
@@ -110,13 +124,15 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     const int m0 = (8 * band + in % rows) * C::BM, n0 = in / rows * C::BN;
 
     const uint8_t *xb = reinterpret_cast<const uint8_t *>(a.X) + m0 * a.x_st;
-    uint32_t xo[C::XI], xc[C::XI];
+    uint32_t xo[C::XI];
 #pragma unroll
     for (int q = 0; q < C::XI; ++q) {
         const int r = 8 * (C::XI * w + q) + (lane >> 3);
-        xc[q] = ((lane & 7) ^ xswz(r)) * 16;
-        xo[q] = static_cast<uint32_t>((min(m0 + r, a.M - 1) - m0) * a.x_st) + xc[q];
+        xo[q] = static_cast<uint32_t>((min(m0 + r, a.M - 1) - m0) * a.x_st) + ((lane & 7) ^ xswz(r)) * 16;
     }
+    // 64 in the lanes that load a stage's second half: the same for every q,
+    // since the rows' swizzles differ in the chunk's lowest bit only
+    const uint32_t far = (((lane & 7) ^ (lane >> 3)) & 4) * 16;
     const int last_tile = (a.N - 1) >> 4;
     uint32_t co[C::CI];
 #pragma unroll
@@ -127,18 +143,20 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     }
     const uint32_t lds_base = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds));
-    const int steps = a.K / 64, stages = (steps + 1) / 2;
+    // the block's share of K: stages [first, last); the large tile takes all
+    const int stages = (a.K / 64 + 1) / 2, share = static_cast<int>(blockIdx.y);
+    const int first = MT == 8 ? 0 : share * stages / a.splits, last = MT == 8 ? stages : (share + 1) * stages / a.splits;
+    const int steps = min(a.K / 64, 2 * last) - 2 * first;
 
     // Stage s to its slot; past the last one the last again, so that the
     // number of loads in flight is the same at every wait.  The second half of
     // an odd last stage is not there: its chunks read the first half.
     auto issue = [&](int s, int slot) __attribute__((always_inline)) {
-        s = min(s, stages - 1);
+        s = min(s, last - 1);
         const uint32_t at = lds_base + slot * C::SLOT;
-        const uint32_t cut = (2 * s + 1 < steps) ? 128 : 64;
+        const uint32_t back = far & (2 * s + 1 < a.K / 64 ? 0 : 64);
 #pragma unroll
-        for (int q = 0; q < C::XI; ++q)
-            dma16(xb + s * 128, xc[q] < cut ? xo[q] : xo[q] - 64, at + (C::XI * w + q) * 1024);
+        for (int q = 0; q < C::XI; ++q) dma16(xb + s * 128, xo[q] - back, at + (C::XI * w + q) * 1024);
         const int group = BITS == 4 ? s : BITS == 2 ? s >> 1 : s >> 2;
         const uint8_t *cb = a.packed + group * a.gstride;
         const uint32_t part = BITS == 4 ? 0 : BITS == 2 ? (s & 1) * 32 : (s & 2) * 16;
@@ -158,54 +176,127 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     const uint8_t *cr = lds + C::XB + w * NT * (C::PIECES * 256) + i16 * 16 +
                         (BITS == 4 ? (g >> 1) * 256 + (g & 1) * 8 : BITS == 2 ? g * 4 : (g >> 1) * 4);
 
-    auto step = [&](auto h_c, int s, int slot) __attribute__((always_inline)) {
+    // Operands of a step of 64: activations and the code words.
+    struct Operands {
+        intx4 x[MT];
+        Words<BITS> w[NT];
+    };
+    auto read_codes = [&](auto h_c, int s, int slot, Operands &o) __attribute__((always_inline)) {
         constexpr int H = decltype(h_c)::value;
         const uint8_t *cp = cr + slot * C::SLOT + (BITS == 4 ? H * 512 : BITS == 2 ? H * 256 : H * 8 + (s & 1) * 256);
-        Words<BITS> wd[NT];
-        intx4 x[MT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if constexpr (BITS == 4) {
                 const u32x2 v = *reinterpret_cast<const u32x2 *>(cp + j * (C::PIECES * 256));
-                wd[j] = {v[0], v[1]};
+                o.w[j] = {v[0], v[1]};
             } else {
-                wd[j].w = *reinterpret_cast<const uint32_t *>(cp + j * (C::PIECES * 256));
-                if constexpr (BITS == 1) wd[j].w >>= 16 * (g & 1);
+                o.w[j].w = *reinterpret_cast<const uint32_t *>(cp + j * (C::PIECES * 256));
+                if constexpr (BITS == 1) o.w[j].w >>= 16 * (g & 1);
             }
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const intx4 *>(xr[H] + slot * C::SLOT + i * 2048);
+    };
+    auto read_rows = [&](auto h_c, int slot, int i, Operands &o) __attribute__((always_inline)) {
+        o.x[i] = *reinterpret_cast<const intx4 *>(xr[decltype(h_c)::value] + slot * C::SLOT + i * 2048);
+    };
+    // The products of a step, a column tile at a time.  While one's run, the
+    // next one's codes are decoded (at the end those of `then`, the first of
+    // the step after) and the operands `to` of a later step are read, half H of
+    // stage s: the matrix unit takes 16 cycles a product, time for two of the
+    // decoding's operations and a read.  The scheduler is held to that order.
+    intx4 b;
+    auto multiply = [&](const Operands &o, const Words<BITS> &then, auto h_c, int s, int slot, Operands &to)
+                        __attribute__((always_inline)) {
+        read_codes(h_c, s, slot, to);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const intx4 b = decode(a, wd[j]);
+            const intx4 bn = decode(a, j + 1 < NT ? o.w[j + 1] : then);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, x[i], acc[i][j], 0, 0, 0);
+            for (int i = j * MT / NT; i < (j + 1) * MT / NT; ++i) read_rows(h_c, slot, i, to);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, o.x[i], acc[i][j], 0, 0, 0);
+            b = bn;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a product
+                __builtin_amdgcn_sched_group_barrier(0x100, MT < 8 ? 2 : 1, 0);      // reads
+                __builtin_amdgcn_sched_group_barrier(0x002, MT < 8 ? 4 : 2, 0);      // vector operations
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    constexpr std::integral_constant<int, 0> half0{};
+    constexpr std::integral_constant<int, 1> half1{};
+    auto read_all = [&](auto h_c, int s, int slot, Operands &o) __attribute__((always_inline)) {
+        read_codes(h_c, s, slot, o);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) read_rows(h_c, slot, i, o);
     };
 
 #pragma unroll
-    for (int s = 0; s < P - 1; ++s) issue(s, s);
+    for (int s = 0; s < P; ++s) issue(first + s, s);
+    wait_vmcnt<(P - 1) * (C::XI + C::CI)>();
+    block_barrier();
     int slot = 0;
-    for (int s = 0; s < stages; ++s) {
+    // Every read of the stage in `slot` is done in all waves and the next stage
+    // has landed: the slot takes stage s + P.
+    auto turn = [&](int s) __attribute__((always_inline)) {
         wait_lgkmcnt0();
         wait_vmcnt<(P - 2) * (C::XI + C::CI)>();
         block_barrier();
-        issue(s + P - 1, slot == 0 ? P - 1 : slot - 1);
-        step(std::integral_constant<int, 0>{}, s, slot);
-        if (2 * s + 1 < steps) step(std::integral_constant<int, 1>{}, s, slot);
+        issue(s + P, slot);
+        __builtin_amdgcn_sched_barrier(0);
         slot = slot == P - 1 ? 0 : slot + 1;
+    };
+    if constexpr (MT == 8) {
+        // Operands a step ahead: a stage's first half is multiplied while its
+        // second half's are read, and that one while the next stage's first
+        // are.
+        Operands even, odd;
+        read_all(half0, first, 0, even);
+        b = decode(a, even.w[0]);
+        for (int s = first; s < first + steps / 2; ++s) {
+            multiply(even, odd.w[0], half1, s, slot, odd);
+            turn(s);
+            multiply(odd, even.w[0], half0, s + 1, slot, even);
+        }
+        if (steps & 1) multiply(even, odd.w[0], half0, 0, slot, odd);
+    } else {
+        // A step's products are shorter than a read's way: operands a whole
+        // stage ahead.
+        Operands x0, x1, y0, y1;
+        read_all(half0, first, 0, x0);
+        read_all(half1, first, 0, x1);
+        b = decode(a, x0.w[0]);
+        auto stage = [&](int s, Operands &c0, Operands &c1, Operands &n0, Operands &n1) __attribute__((always_inline)) {
+            turn(s);
+            multiply(c0, c1.w[0], half0, s + 1, slot, n0);
+            multiply(c1, n0.w[0], half1, s + 1, slot, n1);
+        };
+        auto end = [&](Operands &c0, Operands &c1, Operands &n0) __attribute__((always_inline)) {
+            multiply(c0, c1.w[0], half0, last - 1, slot, n0);
+            if (!(steps & 1)) multiply(c1, c1.w[0], half0, last - 1, slot, n0);
+        };
+        int s = first;
+        for (; s + 2 < last; s += 2) {
+            stage(s, x0, x1, y0, y1);
+            stage(s + 1, y0, y1, x0, x1);
+        }
+        if (s + 1 < last) {
+            stage(s, x0, x1, y0, y1);
+            end(y0, y1, x0);
+        } else {
+            end(x0, x1, y0);
+        }
     }
     wait_vmcnt<0>();        // no load is in flight into LDS when the block ends
 
     // The sums through LDS, so that every output line is written whole: MT / 2
     // row tiles at a time, rows 16 bytes further apart than they are long (the
-    // sixteen rows of a write then lie in different banks).
-    constexpr int RS = C::BN * 4 + 16;
-    const int c = (n0 >> 3) + threadIdx.x % (C::BN / 8);
-    float cs[8], cb[8];
-    columns8(a, c, cs, cb);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    // sixteen rows of a write then lie in different banks).  A thread takes the
+    // same eight columns of every TR-th row.
+    constexpr int RS = C::BN * 4 + 16, TC = C::BN / 8, TR = C::THREADS / TC, RT = 8 * MT / TR;
+    const int tc = threadIdx.x % TC, tr = threadIdx.x / TC, c = (n0 >> 3) + tc;
+    auto to_lds = [&](int half) __attribute__((always_inline)) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < MT / 2; ++i)
@@ -213,22 +304,122 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
             for (int j = 0; j < NT; ++j)
                 *reinterpret_cast<intx4 *>(lds + (16 * i + i16) * RS + ((w * NT + j) * 16 + 4 * g) * 4) = acc[half * (MT / 2) + i][j];
         __syncthreads();
-        const int first = m0 + half * (MT / 2) * 16, rows_left = min(8 * MT, a.M - first);
-        if (8 * c < a.N) {
-            with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) {
-                for (int r = threadIdx.x / (C::BN / 8); r < rows_left; r += C::THREADS / (C::BN / 8)) {
-                    int sum[8];
-                    const intx4 *p = reinterpret_cast<const intx4 *>(lds + r * RS + (threadIdx.x % (C::BN / 8)) * 32);
+    };
+    auto sums = [&](int r, int (&sum)[8]) __attribute__((always_inline)) {
+        const intx4 *p = reinterpret_cast<const intx4 *>(lds + r * RS + tc * 32);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum[e] = p[0][e];
-                        sum[4 + e] = p[1][e];
-                    }
-                    finish8<decltype(type)>(a, first + r, c, a.x_scale[first + r], sum, cs, cb);
-                }
-            });
+        for (int e = 0; e < 4; ++e) {
+            sum[e] = p[0][e];
+            sum[4 + e] = p[1][e];
         }
+    };
+    if (MT < 8 && a.splits > 1) {   // the sums as they are, joined by k_a8_join
+        int32_t *out = a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.p_st;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row0 = m0 + half * (MT / 2) * 16;
+            to_lds(half);
+            for (int r = tr; r < min(8 * MT, a.M - row0); r += TR) {
+                const intx4 *p = reinterpret_cast<const intx4 *>(lds + r * RS + tc * 32);
+                intx4 *to = reinterpret_cast<intx4 *>(out + (row0 + r) * a.p_st + 8 * c);
+                if (8 * c < a.p_st) {
+                    to[0] = p[0];
+                    to[1] = p[1];
+                }
+            }
+        }
+        return;
     }
+    float cs[8], cb[8];
+    columns8(a, c, cs, cb);
+    with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) {
+        using T = decltype(type);
+        const T *other = static_cast<const T *>(a.other);
+        T *y = static_cast<T *>(a.Y);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row0 = m0 + half * (MT / 2) * 16, rows = min(8 * MT, a.M - row0);
+            if (n0 + C::BN <= a.N && rows == 8 * MT) {
+                // a whole half: everything that it loads is on its way while
+                // the sums go through LDS
+                Raw8<T> o[RT];
+                float rs[RT];
+#pragma unroll
+                for (int k = 0; k < RT; ++k) {
+                    const int64_t m = row0 + tr + k * TR;
+                    if (other) o[k] = load_whole8(other + m * a.o_st + 8 * c);
+                    rs[k] = a.x_scale[m];
+                }
+                to_lds(half);
+#pragma unroll
+                for (int k = 0; k < RT; ++k) {
+                    int sum[8];
+                    float v[8];
+                    sums(tr + k * TR, sum);
+                    outputs8<T>(a, rs[k], sum, cs, cb, o[k], v);
+                    T *to = y + (row0 + tr + k * TR) * a.y_st + 8 * c;
+                    if (MT == 8 && a.nt) store_whole8<true>(to, v);
+                    else store_whole8(to, v);
+                }
+            } else {
+                to_lds(half);
+                if (8 * c < a.N)
+                    for (int r = tr; r < rows; r += TR) {
+                        int sum[8];
+                        sums(r, sum);
+                        finish8<T>(a, row0 + r, c, a.x_scale[row0 + r], sum, cs, cb);
+                    }
+            }
+        }
+    });
+}
+
+// Split K: the shares' sums added up, and the epilogue.
+__global__ __launch_bounds__(256) void k_a8_join(A8Args a)
+{
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int chunks = static_cast<int>(a.p_st / 8);
+    const int64_t m = at / chunks;
+    const int c = static_cast<int>(at - m * chunks);
+    if (m >= a.M) return;
+    const intx4 *p = reinterpret_cast<const intx4 *>(a.partial + m * a.p_st + 8 * c);
+    const int64_t step = a.M * a.p_st / 4;
+    intx4 lo = p[0], hi = p[1];
+    for (int i = 1; i < a.splits; ++i) {
+        lo += p[i * step];
+        hi += p[i * step + 1];
+    }
+    int sum[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        sum[e] = lo[e];
+        sum[4 + e] = hi[e];
+    }
+    float cs[8], cb[8];
+    columns8(a, c, cs, cb);
+    with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, m, c, a.x_scale[m], sum, cs, cb); });
+}
+
+// How a shape is cut: 128 x 256 tiles where they give every CU one, else 64 x
+// 128 ones (32 x 128 up to 32 rows), with K split while that gives no CU a
+// second block, eight stages a share at least (two blocks a CU: 512 rows, N =
+// K = 4096, 22.9 us against 15.8 unsplit; 64 rows, N = 4096, K = 14336, 19.6
+// against 16.9: the partial sums cost more than the second block brings).
+struct A8Plan {
+    int mt, splits;          // 16-row tiles a block (0: the stream kernel), shares of K
+    int64_t p_st;            // columns of a row of partial sums
+};
+
+inline A8Plan a8_plan(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 16) return {0, 1, 0};
+    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return {8, 1, 0};
+    const int mt = M <= 32 ? 2 : 4;
+    const int64_t blocks = ((M + 16 * mt - 1) / (16 * mt)) * ((N + 127) / 128), stages = (K / 64 + 1) / 2;
+    int64_t splits = 256 / blocks;
+    if (splits > stages / 8) splits = stages / 8;
+    if (splits < 2) return {mt, 1, 0};
+    return {mt, static_cast<int>(splits), (N + 7) / 8 * 8};
 }
 
 template <int BITS, int WN, int MT, int NT, int P>
@@ -238,34 +429,33 @@ pq_status launch_tile(const A8Args &a, hipStream_t s)
     const int mtiles = (a.M + C::BM - 1) / C::BM, ntiles = (a.N + C::BN - 1) / C::BN;
     const int64_t blocks = static_cast<int64_t>(mtiles) * ntiles;
     if (blocks > kMaxBlocks) return PQ_ERR_SHAPE;
-    hipLaunchKernelGGL((k_a8_tile<BITS, WN, MT, NT, P>), dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), 0, s, a, mtiles,
-                       ntiles);
+    hipLaunchKernelGGL((k_a8_tile<BITS, WN, MT, NT, P>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.splits)),
+                       dim3(C::THREADS), 0, s, a, mtiles, ntiles);
+    if (hipGetLastError() != hipSuccess) return PQ_ERR_HIP;
+    if (a.splits == 1) return PQ_OK;
+    const int64_t threads = a.M * (a.p_st / 8);
+    hipLaunchKernelGGL(k_a8_join, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
 template <int BITS>
-pq_status launch_a8(const A8Args &a, hipStream_t s)
+pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
 {
-    const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
-    if (a.M <= 16) {
-        hipLaunchKernelGGL((k_a8_stream<BITS, 1>), dim3(tiles), dim3(256), 0, s, a);
+    if (plan.mt == 0) {
+        const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
+        constexpr int U = BITS == 1 ? 1 : 2;
+        // Two column tiles a block halve the reads of the activations, where
+        // they are several rows and there is a block for every CU all the same
+        // (16 rows, N = 14336, K = 4096: 7.8 us against 10.8).
+        if (a.M > 4 && tiles >= 512)
+            hipLaunchKernelGGL((k_a8_stream<BITS, 2, U>), dim3((tiles + 1) / 2), dim3(512), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_a8_stream<BITS, 1, U>), dim3(tiles), dim3(512), 0, s, a);
         return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
     }
-    if (a.M >= 128) return launch_tile<BITS, 4, 8, 4, BITS == 4 ? 2 : 3>(a, s);
-    A8Args b = a;
-    // grid rows are counted in 16 bits: more rows go in several launches
-    constexpr int64_t kStep = 65535 * 64;
-    for (int64_t m = 0; m < a.M; m += kStep) {
-        b.M = static_cast<int>(a.M - m < kStep ? a.M - m : kStep);
-        b.X = a.X + m * a.x_st;
-        b.x_scale = a.x_scale + m;
-        const int size = a.y_dtype == PQ_F32 ? 4 : 2;
-        b.Y = static_cast<char *>(a.Y) + m * a.y_st * size;
-        b.other = a.other ? static_cast<const char *>(a.other) + m * a.o_st * size : nullptr;
-        hipLaunchKernelGGL((k_a8_stream<BITS, 4>), dim3(tiles, static_cast<unsigned>((b.M + 63) / 64)), dim3(256), 0, s, b);
-        if (hipGetLastError() != hipSuccess) return PQ_ERR_HIP;
-    }
-    return PQ_OK;
+    if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 4>(a, s);
+    if (plan.mt == 4) return launch_tile<BITS, 4, 4, 2, 4>(a, s);
+    return launch_tile<BITS, 4, 8, 4, BITS == 4 ? 2 : 3>(a, s);
 }
 
 inline bool a8_shape_ok(int mode, int64_t M, int64_t N, int64_t K)
@@ -277,7 +467,7 @@ inline bool a8_shape_ok(int mode, int64_t M, int64_t N, int64_t K)
 inline void set_levels(A8Args &a, int mode)
 {
     auto lut = [&](int l0, int l1, int l2, int l3, float unit) {
-        a.lut_lo = a.lut_hi = (l0 & 255u) | (l1 & 255u) << 8 | (l2 & 255u) << 16 | (l3 & 255u) << 24;
+        a.lut = (l0 & 255u) | (l1 & 255u) << 8 | (l2 & 255u) << 16 | (l3 & 255u) << 24;
         a.unit = unit;
     };
     switch (mode) {
@@ -307,7 +497,10 @@ extern "C" {
 
 int64_t pq_gemm_a8_workspace_bytes(int mode, int64_t M, int64_t N, int64_t K)
 {
-    return pq::a8_shape_ok(mode, M, N, K) ? 0 : -1;
+    if (!pq::a8_shape_ok(mode, M, N, K)) return -1;
+    if (M == 0 || N == 0) return 0;
+    const pq::A8Plan p = pq::a8_plan(M, N, K);
+    return p.splits > 1 ? p.splits * M * p.p_st * 4 : 0;
 }
 
 pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t x_stride,
@@ -356,9 +549,15 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
     a.act = e.activation;
     a.mul = e.other && e.combine == PQ_COMBINE_MUL;
     set_levels(a, mode);
+    const A8Plan plan = a8_plan(M, N, K);
+    a.splits = plan.splits;
+    a.p_st = plan.p_st;
+    // An output of half the memory-side cache's size and more is not written
+    // into the caches.
+    a.nt = M * N * size >= (int64_t(1) << 27);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const int bits = code_bits(mode);
-    return bits == 1 ? launch_a8<1>(a, s) : bits == 2 ? launch_a8<2>(a, s) : launch_a8<4>(a, s);
+    return bits == 1 ? launch_a8<1>(a, plan, s) : bits == 2 ? launch_a8<2>(a, plan, s) : launch_a8<4>(a, plan, s);
 }
 
 }  // extern "C"

@@ -20,13 +20,13 @@ struct A8Args {
     const uint8_t *packed;   // export byte order
     const void *alpha, *bias, *other;
     void *Y;
-    int32_t *partial;        // split K: [splits, M, N]
-    int64_t x_st, y_st, o_st, gstride;
+    int32_t *partial;        // split K: [splits, M, p_st]
+    int64_t x_st, y_st, o_st, p_st, gstride;
     int M, N, K;
     int alpha_dtype, bias_dtype, y_dtype, act, mul;   // mul: multiply by other
-    int splits;
+    int splits, nt;          // shares of K; stores past the caches
     float unit;              // level = unit * decoded int8
-    uint32_t lut_lo, lut_hi;             // 1, 2 bits: level of code c in byte c
+    uint32_t lut;            // 1, 2 bits: level of code c in byte c
     uint32_t flip, mask;     // 4 bits: code ^ flip, masked, stands in the byte's upper bits
     int up;                  //         shifted left by this
 };
@@ -55,10 +55,10 @@ __device__ __forceinline__ intx4 decode(const A8Args &a, const Words<2> &c)
     const uint32_t e = c.w & 0x03030303u, o = (c.w >> 4) & 0x03030303u;
     const uint32_t f = (c.w >> 2) & 0x03030303u, q = (c.w >> 6) & 0x03030303u;
     intx4 r;
-    r[0] = __builtin_amdgcn_perm(a.lut_lo, a.lut_lo, __builtin_amdgcn_perm(o, e, 0x05010400));
-    r[1] = __builtin_amdgcn_perm(a.lut_lo, a.lut_lo, __builtin_amdgcn_perm(o, e, 0x07030602));
-    r[2] = __builtin_amdgcn_perm(a.lut_lo, a.lut_lo, __builtin_amdgcn_perm(q, f, 0x05010400));
-    r[3] = __builtin_amdgcn_perm(a.lut_lo, a.lut_lo, __builtin_amdgcn_perm(q, f, 0x07030602));
+    r[0] = __builtin_amdgcn_perm(a.lut, a.lut, __builtin_amdgcn_perm(o, e, 0x05010400));
+    r[1] = __builtin_amdgcn_perm(a.lut, a.lut, __builtin_amdgcn_perm(o, e, 0x07030602));
+    r[2] = __builtin_amdgcn_perm(a.lut, a.lut, __builtin_amdgcn_perm(q, f, 0x05010400));
+    r[3] = __builtin_amdgcn_perm(a.lut, a.lut, __builtin_amdgcn_perm(q, f, 0x07030602));
     return r;
 }
 __device__ __forceinline__ intx4 decode(const A8Args &a, const Words<4> &c)
@@ -79,7 +79,7 @@ __device__ __forceinline__ intx4 decode(const A8Args &a, const Words<1> &c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t b = __umul24((c.w >> (4 * i)) & 15u, 0x204081u) & 0x01010101u;
-        r[i] = __builtin_amdgcn_perm(a.lut_lo, a.lut_lo, b);
+        r[i] = __builtin_amdgcn_perm(a.lut, a.lut, b);
     }
     return r;
 }
@@ -122,21 +122,35 @@ __device__ __forceinline__ void columns8(const A8Args &a, int c, float (&cs)[8],
     for (int e = 0; e < 8; ++e) cs[e] *= a.unit;
 }
 
-// Eight outputs of row m, columns 8c .. 8c + 7: scales, bias, activation,
-// other, and the store.
+// Eight outputs of a row: scales, bias, activation, other.
+template <typename T>
+__device__ __forceinline__ void outputs8(const A8Args &a, float row_scale, const int (&sum)[8], const float (&cs)[8],
+                                         const float (&cb)[8], const Raw8<T> &other, float (&v)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(static_cast<float>(sum[e]), row_scale * cs[e], cb[e]);
+    activate(v, a.act);
+    if (!a.other) return;
+    float o[8];
+    raw_to_f32<T>(other, o);
+    if (a.mul) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= o[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += o[e];
+    }
+}
+
+// Eight outputs of row m, columns 8c .. 8c + 7 (those below N), and the store.
 template <typename T>
 __device__ __forceinline__ void finish8(const A8Args &a, int64_t m, int c, float row_scale, const int (&sum)[8], const float (&cs)[8],
                                         const float (&cb)[8])
 {
-    float v[8], o[8];
-    if (a.other) raw_to_f32<T>(load_row8(static_cast<const T *>(a.other) + m * a.o_st, c, a.N), o);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(static_cast<float>(sum[e]), row_scale * cs[e], cb[e]);
-    activate(v, a.act);
-    if (a.other) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = a.mul ? v[e] * o[e] : v[e] + o[e];
-    }
+    float v[8];
+    Raw8<T> other;
+    if (a.other) other = load_row8(static_cast<const T *>(a.other) + m * a.o_st, c, a.N);
+    outputs8<T>(a, row_scale, sum, cs, cb, other, v);
     store_row8<T>(static_cast<T *>(a.Y) + m * a.y_st, c, a.N, v);
 }
 

@@ -19,6 +19,15 @@ typedef u32x4 u32x4_a1 __attribute__((aligned(1)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
 
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_whole8(const T *p)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const u32x4_a1 *>(p)[i];
+    return r;
+}
+
 // Elements 8c .. 8c + 7 of a row of `cols`, as they lie in memory; those past
 // its end are zero.
 template <typename T>
@@ -26,11 +35,7 @@ __device__ __forceinline__ Raw8<T> load_row8(const T *row, int c, int cols)
 {
     Raw8<T> r;
     const T *p = row + 8 * static_cast<int64_t>(c);
-    if (8 * c + 8 <= cols) {
-#pragma unroll
-        for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const u32x4_a1 *>(p)[i];
-        return r;
-    }
+    if (8 * c + 8 <= cols) return load_whole8(p);
 #pragma unroll
     for (unsigned i = 0; i < sizeof(T) / 2; ++i) r.w[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -45,27 +50,33 @@ __device__ __forceinline__ Raw8<T> load_row8(const T *row, int c, int cols)
     return r;
 }
 
+template <bool NT = false, typename T>
+__device__ __forceinline__ void store_whole8(T *p, const float (&x)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const f32x4 v[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
+        f32x4_a4 *to = reinterpret_cast<f32x4_a4 *>(p);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if constexpr (NT) __builtin_nontemporal_store(v[i], to + i);
+            else to[i] = v[i];
+        }
+    } else {
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = pack16<T>(x[2 * e], x[2 * e + 1]);
+        u32x4_a1 *to = reinterpret_cast<u32x4_a1 *>(p);
+        if constexpr (NT) __builtin_nontemporal_store(v, to);
+        else *to = v;
+    }
+}
+
 template <typename T, bool NT = false>
 __device__ __forceinline__ void store_row8(T *row, int c, int cols, const float (&x)[8])
 {
     T *p = row + 8 * static_cast<int64_t>(c);
     if (8 * c + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            const f32x4 v[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
-            f32x4_a4 *to = reinterpret_cast<f32x4_a4 *>(p);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if constexpr (NT) __builtin_nontemporal_store(v[i], to + i);
-                else to[i] = v[i];
-            }
-        } else {
-            u32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = pack16<T>(x[2 * e], x[2 * e + 1]);
-            u32x4_a1 *to = reinterpret_cast<u32x4_a1 *>(p);
-            if constexpr (NT) __builtin_nontemporal_store(v, to);
-            else *to = v;
-        }
+        store_whole8<NT>(p, x);
         return;
     }
 #pragma unroll
