@@ -8,7 +8,10 @@
 // sums exp against the maximum of its own words and the (maximum, sum) pairs
 // are joined once, so there is one reduction a row; rows of up to 131072 words
 // of 16 bits (65536 of fp32) stay in registers between the sum and the
-// gradient, longer ones are read a second time.
+// gradient, longer ones are read a second time.  One wave reads the teacher's
+// list while the others read the row.
+// 2048 rows of 128256 words in bf16 take 208 us, 5.06 TB/s, the rate of a copy;
+// the gradient by itself 206.
 //
 // p is 0 for all but k words.  The entries stand in LDS as chains hashed by
 // chunks of eight words: a thread looks at one head per chunk and walks a
@@ -26,6 +29,7 @@ namespace {
 
 constexpr int kMaxTop = 1024;
 constexpr int kHeads = 1024;            // heads of the chains
+constexpr int U = 4;                    // chunks in flight a thread, where a row is not kept
 
 struct DistillArgs {
     const void *z, *top;
@@ -35,6 +39,7 @@ struct DistillArgs {
     float *loss, *stats;
     int64_t z_st, d_st;
     int rows, vocab, k, top_dtype, segment;
+    int nt;                             // the gradient is not written into the caches
     float temp, inv_temp, c;            // c = log2(e) / T
     double grad;                        // grad_scale T
 };
@@ -59,93 +64,80 @@ __device__ __forceinline__ double wave_sum64(double x)
     return x;
 }
 
-// The teacher's entries of a row in LDS.
+// The teacher's entries of a row in LDS, and what the waves of a block tell
+// each other.
 struct Entries {
     int32_t word[kMaxTop];              // -1: does not count
     float p[kMaxTop];                   // exp((t - max) / T), not yet divided by its sum
+    float all[kMaxTop];                 // a word's p: its first entry's, 0 in the word's others
     int16_t next[kMaxTop];
-    int head[kHeads];                   // first entry of a chain, -1
-    float red[16];
-    double red64[16];
+    int32_t head[kHeads];               // first entry of a chain, -1
+    double total, dot;                  // sum of p; sum of p (t - max - z)
+    float most[16], sum[16];            // of the waves' words
 };
 
-template <int TEAM>
-__device__ __forceinline__ float team_fmax(float x, Entries &l)
-{
-    x = wave_fmax(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) l.red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = l.red[0];
-#pragma unroll
-    for (int i = 1; i < TEAM / 64; ++i) x = fmaxf(x, l.red[i]);
-    return x;
-}
-template <int TEAM>
-__device__ __forceinline__ double team_sum64(double x, Entries &l)
-{
-    x = wave_sum64(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) l.red64[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = l.red64[0];
-#pragma unroll
-    for (int i = 1; i < TEAM / 64; ++i) x += l.red64[i];
-    return x;
-}
+// Between accesses of one wave's lanes to what its other lanes wrote.
+__device__ __forceinline__ void lanes_agree() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-// Entries of row r to LDS: words and exp((t - max) / T); max and the sum of p
-// come back, sum 0 where no entry counts.  A NaN among the counting logits
-// makes the sum NaN.
-template <int TEAM>
-__device__ __forceinline__ void read_entries(const DistillArgs &a, int64_t r, Entries &l, float &top, double &total)
+// One wave's work, while the others read the row: the entries of row r, their
+// sum (0 where none counts or all are -inf, NaN where one is NaN), the loss's
+// sum with the entries' own logits and, for a gradient, the chains.
+template <typename T>
+__device__ __forceinline__ void read_entries(const DistillArgs &a, int64_t r, const T *z, bool loss, bool chains, Entries &l)
 {
+    const int lane = threadIdx.x & 63;
     float most = -INFINITY;
-    for (int j = threadIdx.x; j < a.k; j += TEAM) {
+    for (int j = lane; j < a.k; j += 64) {
         const int w = a.index[r * a.k + j];
+        const float t = load_any(a.top, a.top_dtype, r * a.k + j);
         const bool counts = w >= 0 && w < a.vocab;
-        const float t = counts ? load_any(a.top, a.top_dtype, r * a.k + j) : -INFINITY;
         l.word[j] = counts ? w : -1;
         l.p[j] = t;
-        most = fmaxf(most, t);
+        if (counts) most = fmaxf(most, t);
     }
-    top = team_fmax<TEAM>(most, l);
-    const float ref = top == -INFINITY ? 0.f : top;
-    double s = 0.0;
-    for (int j = threadIdx.x; j < a.k; j += TEAM) {
-        const float p = __builtin_amdgcn_exp2f((l.p[j] - ref) * a.c);
-        l.p[j] = l.word[j] < 0 ? 0.f : p;
-        s += l.p[j];
-    }
-    total = team_sum64<TEAM>(s, l);
-}
-
-// The chains: every word once, with the sum of its entries' p.
-template <int TEAM>
-__device__ __forceinline__ void chain_entries(const DistillArgs &a, Entries &l)
-{
-    for (int i = threadIdx.x; i < kHeads; i += TEAM) l.head[i] = -1;
-    __syncthreads();
-    for (int j = threadIdx.x; j < a.k; j += TEAM) {
+    if (chains)
+        for (int i = lane; i < kHeads; i += 64) l.head[i] = -1;
+    const float top = wave_fmax(most), ref = top == -INFINITY ? 0.f : top;
+    lanes_agree();
+    double total = 0.0, dot = 0.0;
+    for (int j = lane; j < a.k; j += 64) {
         const int w = l.word[j];
-        if (w < 0) continue;
-        bool first = true;
-        for (int i = 0; i < j && first; ++i) first = l.word[i] != w;
-        if (first) l.next[j] = static_cast<int16_t>(atomicExch(&l.head[(w >> 3) & (kHeads - 1)], j));
+        const float t = l.p[j], p = w < 0 ? 0.f : __builtin_amdgcn_exp2f((t - ref) * a.c);
+        l.p[j] = p;
+        total += p;
+        if (loss && p != 0.f) dot += static_cast<double>(p) * (static_cast<double>(t) - ref - static_cast<double>(to_f32(z[w])));
+        // p = 0 needs no place in a chain: lists filled up with one word stay short
+        if (chains && p != 0.f) l.next[j] = static_cast<int16_t>(atomicExch(&l.head[(w >> 3) & (kHeads - 1)], j));
     }
-    __syncthreads();
+    total = wave_sum64(total);
+    dot = wave_sum64(dot);
+    if (lane == 0) {
+        l.total = total;
+        l.dot = dot;
+    }
+    if (!chains) return;
+    lanes_agree();
+    // A word that is named more than once: its first entry takes the sum.  It
+    // is one of whole numbers (of 2^-50; the list's largest p is 1), so that
+    // the chain's order, which is chance, does not show.
+    for (int j = lane; j < a.k; j += 64) {
+        float p = l.p[j];
+        if (p == 0.f) continue;
+        const int w = l.word[j];
+        bool first = true, more = false;
+        uint64_t sum = 0;
+        for (int i = l.head[(w >> 3) & (kHeads - 1)]; i >= 0; i = l.next[i]) {
+            if (l.word[i] != w) continue;
+            first = first && i >= j;
+            more = more || i != j;
+            sum += static_cast<uint64_t>(static_cast<double>(l.p[i]) * 0x1p50);
+        }
+        if (more) p = first ? static_cast<float>(static_cast<double>(sum) * 0x1p-50) : 0.f;
+        l.all[j] = p;
+    }
 }
 
-// Sum of p over the entries of a word, in the entries' order.
-__device__ __forceinline__ float word_p(const DistillArgs &a, const Entries &l, int j)
-{
-    float p = l.p[j];
-    for (int i = j + 1; i < a.k; ++i)
-        if (l.word[i] == l.word[j]) p += l.p[i];
-    return p;
-}
-
-// Gradient of eight words: g (q - p), q = exp((z - top) / T) inv.
+// Gradient of the eight words of chunk c: g (q - p), q = exp((z - top) / T) / sum.
 template <typename T>
 __device__ __forceinline__ void grad8(const DistillArgs &a, const Entries &l, T *dz, int c, const Raw8<T> &raw, float top,
                                       float gq, float gp)
@@ -156,29 +148,32 @@ __device__ __forceinline__ void grad8(const DistillArgs &a, const Entries &l, T 
     for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f((x[e] - top) * a.c) * gq;
     for (int j = l.head[c & (kHeads - 1)]; j >= 0; j = l.next[j]) {
         if (l.word[j] >> 3 != c) continue;
-        const float p = gp * word_p(a, l, j);
+        const float p = gp * l.all[j];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] -= (l.word[j] & 7) == e ? p : 0.f;
     }
-    store_row8<T>(dz, c, a.vocab, x);
+    if (a.nt) store_whole8<true>(dz + 8 * static_cast<int64_t>(c), x);
+    else store_whole8(dz + 8 * static_cast<int64_t>(c), x);
 }
 
+// Gradient of one word, of those behind the last whole chunk.
 template <typename T>
-__device__ __forceinline__ void zero_row(T *dz, int vocab, int from, int to, int step)
+__device__ __forceinline__ void grad1(const DistillArgs &a, const Entries &l, T *dz, int w, float z, float top, float gq, float gp)
+{
+    float x = __builtin_amdgcn_exp2f((z - top) * a.c) * gq;
+    for (int j = l.head[(w >> 3) & (kHeads - 1)]; j >= 0; j = l.next[j])
+        if (l.word[j] == w) x -= gp * l.all[j];
+    dz[w] = from_f32<T>(x);
+}
+
+// Words 8 from .. of a row to 0, and those behind the last whole chunk where
+// `rest` is theirs.
+template <typename T>
+__device__ __forceinline__ void zero_words(T *dz, int from, int to, int step, int rest, int vocab)
 {
     const float z[8] = {};
-    for (int c = from; c < to; c += step) store_row8<T>(dz, c, vocab, z);
-}
-
-// Words past a row's end stand as -inf: no part of maximum and sum.
-template <typename T>
-__device__ __forceinline__ void words8(const Raw8<T> &raw, int c, int vocab, float (&x)[8])
-{
-    raw_to_f32<T>(raw, x);
-    if (8 * c + 8 > vocab) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 8 * c + e < vocab ? x[e] : -INFINITY;
-    }
+    for (int c = from; c < to; c += step) store_whole8(dz + 8 * static_cast<int64_t>(c), z);
+    if (rest >= 0 && rest < vocab) dz[rest] = from_f32<T>(0.f);
 }
 
 // The compiler would keep a row's fp32 values from one use to the next, twice
@@ -190,98 +185,129 @@ __device__ __forceinline__ void as_read(Raw8<T> &raw)
     for (unsigned i = 0; i < sizeof(T) / 2; ++i) asm volatile("" : "+v"(raw.w[i]));
 }
 
-// NV > 0: the row in registers, NV chunks a thread; NV = 0: read twice.
+// NV > 0: the row in registers, NV chunks a thread; NV = 0: read twice.  The
+// words behind the last whole chunk go to the first threads, one each.
 template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM) void k_distill(DistillArgs a)
 {
     __shared__ Entries l;
     const int64_t r = blockIdx.x;
-    const int tid = threadIdx.x, chunks = (a.vocab + 7) / 8;
+    const int tid = threadIdx.x, chunks = a.vocab / 8, rest = 8 * chunks + tid;
     const T *z = static_cast<const T *>(a.z) + r * a.z_st;
     T *dz = a.dz ? static_cast<T *>(a.dz) + r * a.d_st : nullptr;
     const float weight = a.row_weight ? a.row_weight[r] : 1.f;
     Raw8<T> raw[NV > 0 ? NV : 1];
-    if constexpr (NV > 0) {
-        if (weight != 0.f) {
+    float z_rest = -INFINITY;
+    if (weight != 0.f) {
+        if constexpr (NV > 0) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) raw[v] = load_row8(z, min(tid + v * TEAM, chunks - 1), a.vocab);
+            for (int v = 0; v < NV; ++v)
+                if (tid + v * TEAM < chunks) raw[v] = load_whole8(z + 8 * static_cast<int64_t>(tid + v * TEAM));
+        }
+        if (rest < a.vocab) z_rest = to_f32(z[rest]);
+    }
+    if (tid < 64 && weight != 0.f) read_entries<T>(a, r, z, a.loss != nullptr, dz != nullptr, l);
+    float m = z_rest, s = 0.f;
+    if (weight != 0.f) {
+        if constexpr (NV > 0) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (tid + v * TEAM >= chunks) continue;
+                float x[8];
+                as_read(raw[v]);
+                raw_to_f32<T>(raw[v], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, x[e]);
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (tid + v * TEAM >= chunks) continue;
+                float x[8];
+                as_read(raw[v]);
+                raw_to_f32<T>(raw[v], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
+            }
+            s += __builtin_amdgcn_exp2f((z_rest - ref) * a.c);
+        } else {
+            s = z_rest == -INFINITY ? 0.f : 1.f;
+            for (int c = tid; c < chunks; c += U * TEAM) {
+                Raw8<T> q[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c + u * TEAM >= chunks) break;
+                    float x[8], more = m;
+                    raw_to_f32<T>(q[u], x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) more = fmaxf(more, x[e]);
+                    const float ref = more == -INFINITY ? 0.f : more;
+                    s *= __builtin_amdgcn_exp2f((m - ref) * a.c);
+                    m = more;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
+                }
+            }
         }
     }
-    float t_top;
-    double t_sum = 0.0;
-    if (weight != 0.f) read_entries<TEAM>(a, r, l, t_top, t_sum);
+    // the pairs (maximum, sum) of the lanes, then of the waves
+    float top = wave_fmax(m), ref = top == -INFINITY ? 0.f : top;
+    s = wave_sum(s * __builtin_amdgcn_exp2f((m - ref) * a.c));
+    if ((tid & 63) == 0) {
+        l.most[tid >> 6] = top;
+        l.sum[tid >> 6] = s;
+    }
+    __syncthreads();
+    const double t_sum = weight != 0.f ? l.total : 0.0;
     if (t_sum == 0.0) {                 // nothing to learn from: the same for the whole block
         if (tid == 0 && a.loss) a.loss[r] = 0.f;
         if (tid < 2 && a.stats) a.stats[2 * r + tid] = static_cast<float>(tid);
-        if (dz) zero_row(dz, a.vocab, tid, chunks, TEAM);
+        if (dz) zero_words(dz, tid, chunks, TEAM, rest, a.vocab);
         return;
     }
-    // the entries' own logits, before any of them may be overwritten
-    double dot = 0.0;
-    for (int j = tid; j < a.k; j += TEAM) {
-        const float p = l.p[j];
-        if (p == 0.f) continue;
-        // T ln(p / max p): the teacher's logit below its best, from p's own argument
-        const float t = load_any(a.top, a.top_dtype, r * a.k + j) - t_top;
-        dot += static_cast<double>(p) * (static_cast<double>(t) - static_cast<double>(to_f32(z[l.word[j]])));
-    }
-    float m = -INFINITY, s = 0.f;
-    if constexpr (NV > 0) {
+    top = l.most[0];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float x[8];
-            words8<T>(raw[v], tid + v * TEAM, a.vocab, x);
+    for (int i = 1; i < TEAM / 64; ++i) top = fmaxf(top, l.most[i]);
+    ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, x[e]);
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float x[8];
-            as_read(raw[v]);
-            words8<T>(raw[v], tid + v * TEAM, a.vocab, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
-        }
-    } else {
-        for (int c = tid; c < chunks; c += TEAM) {
-            float x[8], more = m;
-            words8<T>(load_row8(z, c, a.vocab), c, a.vocab, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) more = fmaxf(more, x[e]);
-            const float ref = more == -INFINITY ? 0.f : more;
-            s *= __builtin_amdgcn_exp2f((m - ref) * a.c);
-            m = more;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
-        }
-    }
-    const float top = team_fmax<TEAM>(m, l), ref = top == -INFINITY ? 0.f : top;
-    const double sum = team_sum64<TEAM>(static_cast<double>(s * __builtin_amdgcn_exp2f((m - ref) * a.c)), l);
-    dot = team_sum64<TEAM>(dot, l);
+    for (int i = 0; i < TEAM / 64; ++i) sum += l.sum[i] * __builtin_amdgcn_exp2f((l.most[i] - ref) * a.c);
     if (tid == 0) {
         if (a.stats) {
             a.stats[2 * r] = top;
-            a.stats[2 * r + 1] = static_cast<float>(sum);
+            a.stats[2 * r + 1] = sum;
         }
         if (a.loss) {
-            const double kl = (dot / t_sum + static_cast<double>(top)) * a.inv_temp + log(sum) - log(t_sum);
+            const double kl = (l.dot / t_sum + static_cast<double>(top)) * a.inv_temp + log(static_cast<double>(sum)) - log(t_sum);
             a.loss[r] = static_cast<float>(kl * weight * a.temp * a.temp);
         }
     }
     if (!dz) return;
-    chain_entries<TEAM>(a, l);
     const double g = a.grad * weight;
-    const float gq = static_cast<float>(g / sum), gp = static_cast<float>(g / t_sum);
+    const float gq = static_cast<float>(g / static_cast<double>(sum)), gp = static_cast<float>(g / t_sum);
     if constexpr (NV > 0) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (tid + v * TEAM >= chunks) continue;
             as_read(raw[v]);
-            if (tid + v * TEAM < chunks) grad8<T>(a, l, dz, tid + v * TEAM, raw[v], top, gq, gp);
+            grad8<T>(a, l, dz, tid + v * TEAM, raw[v], top, gq, gp);
         }
     } else {
-        for (int c = tid; c < chunks; c += TEAM) grad8<T>(a, l, dz, c, load_row8(z, c, a.vocab), top, gq, gp);
+        for (int c = tid; c < chunks; c += U * TEAM) {
+            Raw8<T> q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c + u * TEAM < chunks) grad8<T>(a, l, dz, c + u * TEAM, q[u], top, gq, gp);
+        }
     }
+    if (rest < a.vocab) grad1<T>(a, l, dz, rest, z_rest, top, gq, gp);
 }
 
 // The gradient by itself: blocks of `segment` chunks of a row.
@@ -290,36 +316,46 @@ __global__ __launch_bounds__(512) void k_distill_bwd(DistillArgs a)
 {
     __shared__ Entries l;
     const int64_t r = blockIdx.x;
-    const int chunks = (a.vocab + 7) / 8;
+    const int chunks = a.vocab / 8;
     const int from = static_cast<int>(blockIdx.y) * a.segment, to = min(from + a.segment, chunks);
+    const int rest = to == chunks ? 8 * chunks + static_cast<int>(threadIdx.x) : -1;
     const T *z = static_cast<const T *>(a.z) + r * a.z_st;
     T *dz = static_cast<T *>(a.dz) + r * a.d_st;
     const float weight = a.row_weight ? a.row_weight[r] : 1.f;
-    float t_top;
-    double t_sum = 0.0;
-    if (weight != 0.f) read_entries<512>(a, r, l, t_top, t_sum);
+    if (threadIdx.x < 64 && weight != 0.f) read_entries<T>(a, r, z, false, true, l);
+    __syncthreads();
+    const double t_sum = weight != 0.f ? l.total : 0.0;
     if (t_sum == 0.0) {
-        zero_row(dz, a.vocab, from + static_cast<int>(threadIdx.x), to, 512);
+        zero_words(dz, from + static_cast<int>(threadIdx.x), to, 512, rest, a.vocab);
         return;
     }
-    chain_entries<512>(a, l);
     const double g = a.grad * weight * a.dloss[r];
     const float top = a.stats_in[2 * r];
     const float gq = static_cast<float>(g / a.stats_in[2 * r + 1]), gp = static_cast<float>(g / t_sum);
-    for (int c = from + static_cast<int>(threadIdx.x); c < to; c += 512)
-        grad8<T>(a, l, dz, c, load_row8(z, c, a.vocab), top, gq, gp);
+    for (int c = from + static_cast<int>(threadIdx.x); c < to; c += U * 512) {
+        Raw8<T> q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * 512, to - 1)));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c + u * 512 < to) grad8<T>(a, l, dz, c + u * 512, q[u], top, gq, gp);
+    }
+    if (rest >= 0 && rest < a.vocab) grad1<T>(a, l, dz, rest, to_f32(z[rest]), top, gq, gp);
 }
 
+// A row stays in registers where it fits.  (For the loss alone rows over 65536
+// words would be read faster twice over, with two blocks a CU in place of one:
+// 2048 rows of 128256 words in bf16 93 us against 108; with the gradient 262
+// against 218.  One form for both gives one loss, bit for bit.)
 template <typename T>
 pq_status launch_distill(const DistillArgs &a, hipStream_t s)
 {
     const dim3 grid(static_cast<unsigned>(a.rows));
-    constexpr int WORDS = sizeof(T) == 4 ? 8 : 16;      // most chunks a thread keeps
     if (a.vocab <= 256 * 8 * 4) hipLaunchKernelGGL((k_distill<T, 256, 4>), grid, dim3(256), 0, s, a);
     else if (a.vocab <= 512 * 8 * 8) hipLaunchKernelGGL((k_distill<T, 512, 8>), grid, dim3(512), 0, s, a);
     else if (a.vocab <= 1024 * 8 * 8) hipLaunchKernelGGL((k_distill<T, 1024, 8>), grid, dim3(1024), 0, s, a);
-    else if (WORDS > 8 && a.vocab <= 1024 * 8 * WORDS)
-        hipLaunchKernelGGL((k_distill<T, 1024, WORDS>), grid, dim3(1024), 0, s, a);
+    else if (sizeof(T) == 2 && a.vocab <= 1024 * 8 * 16)
+        hipLaunchKernelGGL((k_distill<T, 1024, sizeof(T) == 2 ? 16 : 0>), grid, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL((k_distill<T, 1024, 0>), grid, dim3(1024), 0, s, a);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
@@ -357,6 +393,10 @@ inline pq_status distill_args(DistillArgs &a, int dtype, int64_t rows, int64_t v
     a.temp = temp;
     a.inv_temp = inv;
     a.c = static_cast<float>(1.4426950408889634074 / temperature);
+    // Half the memory-side cache's size and more is written past the caches
+    // (2048 x 128256 in bf16 208 us against 218, 512 x 200000 103 against 119);
+    // less may be found there by its reader (517 x 32003 in fp32 28 against 41).
+    a.nt = rows * vocab * size > (int64_t(1) << 27);
     return PQ_OK;
 }
 
@@ -404,11 +444,12 @@ pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *log
     a.stats_in = stats;
     a.dloss = dloss;
     a.grad = temperature;
-    const int64_t chunks = (vocab + 7) / 8;
+    const int64_t chunks = vocab / 8 > 0 ? vocab / 8 : 1;
     // up to 65535 blocks a row, of 4096 words and more
     int64_t segments = (chunks + 4095) / 4096;
     if (segments > 65535) segments = 65535;
     a.segment = static_cast<int>((chunks + segments - 1) / segments);
+    segments = (chunks + a.segment - 1) / a.segment;
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(segments));
     const hipStream_t s = static_cast<hipStream_t>(stream);
     if (dtype == PQ_F32) hipLaunchKernelGGL(k_distill_bwd<float>, grid, dim3(512), 0, s, a);
