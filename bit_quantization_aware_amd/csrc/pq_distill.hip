@@ -176,15 +176,6 @@ __device__ __forceinline__ void zero_words(T *dz, int from, int to, int step, in
     if (rest >= 0 && rest < vocab) dz[rest] = from_f32<T>(0.f);
 }
 
-// The compiler would keep a row's fp32 values from one use to the next, twice
-// the registers of 16-bit words: it is told that they may have changed.
-template <typename T>
-__device__ __forceinline__ void as_read(Raw8<T> &raw)
-{
-#pragma unroll
-    for (unsigned i = 0; i < sizeof(T) / 2; ++i) asm volatile("" : "+v"(raw.w[i]));
-}
-
 // NV > 0: the row in registers, NV chunks a thread; NV = 0: read twice.  The
 // words behind the last whole chunk go to the first threads, one each.
 template <typename T, int TEAM, int NV>

@@ -212,6 +212,11 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float n[8], g[8];
+            if constexpr (WIDE) {
+                __builtin_amdgcn_sched_barrier(0);
+                as_read(rh[v]);
+                as_read(rd[v]);
+            }
             raw_to_f32<T>(rh[v], n);
             raw_to_f32<T>(rd[v], g);
             if constexpr (WIDE) load_any8(a.weight, a.w_dtype, tid + v * TEAM, cols, w[0]);
@@ -228,6 +233,11 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float n[8], g[8], s[8] = {};
+            if constexpr (WIDE) {
+                __builtin_amdgcn_sched_barrier(0);
+                as_read(rh[v]);
+                as_read(rd[v]);
+            }
             raw_to_f32<T>(rh[v], n);
             raw_to_f32<T>(rd[v], g);
             if constexpr (WIDE) load_any8(a.weight, a.w_dtype, tid + v * TEAM, cols, w[0]);
@@ -238,28 +248,48 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
         }
     }
     if (!a.partial) return;
-    float *out = a.partial + team * cols;
+    if constexpr (TEAM == 64) {             // the four waves of a block share a row of partial sums
+        __shared__ float rows[4][64 * NV * 8];
+        float *mine = rows[threadIdx.x >> 6];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) store_row8<float>(out, tid + v * TEAM, cols, dw[v]);
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mine[(tid + v * 64) * 8 + e] = dw[v][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += 256)
+            a.partial[static_cast<int64_t>(blockIdx.x) * cols + c] = (rows[0][c] + rows[1][c]) + (rows[2][c] + rows[3][c]);
+    } else {
+        float *out = a.partial + team * cols;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) store_row8<float>(out, tid + v * TEAM, cols, dw[v]);
+    }
 }
 
-// dweight: the partial rows added up, 64 columns a block, sixteen strided sums
-// side by side and then one after the other (always in this order).
+// dweight: the partial rows added up, 16 columns a block, 64 strided sums side
+// by side, each with eight loads in flight, joined in a fixed order.
 __global__ __launch_bounds__(1024) void k_norm_dweight(const float *partial, int64_t parts, int cols, float *dweight)
 {
-    __shared__ float lds[16][64];
-    const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    __shared__ float lds[64][17];
+    const int lane = threadIdx.x & 15, g = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + lane;
     float s = 0.f;
     if (c < cols)
-        for (int64_t p = g; p < parts; p += 16) s += partial[p * cols + c];
+        for (int64_t p0 = g; p0 < parts; p0 += 64 * 8) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = p0 + 64 * u < parts ? partial[(p0 + 64 * u) * cols + c] : 0.f;
+            s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        }
     lds[g][lane] = s;
     __syncthreads();
-    if (g == 0 && c < cols) {
+    if (threadIdx.x >= 64) return;
+    // one wave: 4 partial sums of 16 each a column, then two steps over the lanes
+    s = 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += lds[i][lane];
-        dweight[c] = s;
-    }
+    for (int i = 0; i < 16; ++i) s += lds[16 * g + i][lane];
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (g == 0 && c < cols) dweight[c] = s;
 }
 
 // Team and chunks of a row: one wave up to 1024 columns, then 256 threads up
@@ -308,17 +338,15 @@ pq_status launch_norm(const NormArgs &a, hipStream_t s)
     });
 }
 
-// Teams of the gradient: as many as the chip holds at once (256 threads: two
-// blocks a CU), each with a row of partial sums.
-inline int64_t bwd_teams(int64_t rows, int64_t cols)
+// Blocks of the gradient, each with a row of partial sums: two of 256 threads a
+// CU and four of waves that take a row each (16384 x 4096 in bf16 with 256, 512,
+// 768, 1024 blocks 116, 103, 107, 111 us; 65536 x 576 with 512, 1024, 1792,
+// 2048 99, 68, 76, 71).
+inline int64_t bwd_blocks(int64_t rows, int64_t cols)
 {
-    const int64_t most = team_of(cols) == 64 ? 4096 : team_of(cols) == 256 ? 1024 : 256;
-    return rows < most ? rows : most;
-}
-inline int64_t bwd_partials(int64_t rows, int64_t cols)
-{
-    const int64_t t = bwd_teams(rows, cols);
-    return team_of(cols) == 64 ? (t + 3) / 4 * 4 : t;
+    const int team = team_of(cols);
+    const int64_t need = team == 64 ? (rows + 3) / 4 : rows, most = team == 64 ? 1024 : team == 256 ? 512 : 256;
+    return need < most ? need : most;
 }
 
 template <typename T>
@@ -327,7 +355,7 @@ pq_status launch_norm_bwd(const NormBwdArgs &a, hipStream_t s)
     return with_shape(a.cols, [&](auto team, auto nv) {
         constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
         if constexpr (TEAM * NV * 8 <= kMaxNormCols) {
-            hipLaunchKernelGGL((k_norm_bwd<T, TEAM, NV>), dim3(team_blocks(bwd_teams(a.rows, a.cols), TEAM)),
+            hipLaunchKernelGGL((k_norm_bwd<T, TEAM, NV>), dim3(static_cast<unsigned>(bwd_blocks(a.rows, a.cols))),
                                dim3(TEAM < 256 ? 256 : TEAM), 0, s, a);
             return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
         } else {
@@ -389,7 +417,7 @@ int64_t pq_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols)
 {
     using namespace pq;
     if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > kMaxNormCols) return -1;
-    return (bwd_partials(rows, cols) * cols * 4 + 15) / 16 * 16;
+    return (bwd_blocks(rows, cols) * cols * 4 + 15) / 16 * 16;
 }
 
 pq_status pq_rmsnorm_bwd(int dtype, int64_t rows, int64_t cols, const void *h, int64_t h_stride, const void *weight,
@@ -432,8 +460,8 @@ pq_status pq_rmsnorm_bwd(int dtype, int64_t rows, int64_t cols, const void *h, i
         if (rc != PQ_OK) return rc;
     }
     if (dweight) {
-        hipLaunchKernelGGL(k_norm_dweight, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(1024), 0, s,
-                           static_cast<const float *>(workspace), bwd_partials(rows, cols), static_cast<int>(cols), dweight);
+        hipLaunchKernelGGL(k_norm_dweight, dim3(static_cast<unsigned>((cols + 15) / 16)), dim3(1024), 0, s,
+                           static_cast<const float *>(workspace), bwd_blocks(rows, cols), static_cast<int>(cols), dweight);
         if (hipGetLastError() != hipSuccess) return PQ_ERR_HIP;
     }
     return PQ_OK;

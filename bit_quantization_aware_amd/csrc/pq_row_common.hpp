@@ -28,6 +28,15 @@ __device__ __forceinline__ Raw8<T> load_whole8(const T *p)
     return r;
 }
 
+// The compiler would keep a row's fp32 values from one use to the next, twice
+// the registers of 16-bit words: it is told that they may have changed.
+template <typename T>
+__device__ __forceinline__ void as_read(Raw8<T> &raw)
+{
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 2; ++i) asm volatile("" : "+v"(raw.w[i]));
+}
+
 // Elements 8c .. 8c + 7 of a row of `cols`, as they lie in memory; those past
 // its end are zero.
 template <typename T>

@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -643,6 +644,7 @@ def pq_attn_decode(cache: KVCache, q, block_table, lens, out, lse=None, scale=No
 
 PQ_ACT_NONE, PQ_ACT_RELU, PQ_ACT_SILU, PQ_ACT_GELU, PQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
 PQ_COMBINE_ADD, PQ_COMBINE_MUL = 0, 1
+_EPILOGUE = struct.Struct("PPqiiii")         # pq_epilogue; packed, it costs a call a quarter of what its fields do
 
 
 def _device(t: torch.Tensor, what: str) -> int:
@@ -653,9 +655,16 @@ def _device(t: torch.Tensor, what: str) -> int:
     return d
 
 
+def _launch_stream(stream, device: int) -> Optional[int]:
+    """_stream where the current device is known."""
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(device)
+    return _stream(stream)
+
+
 def _matrix(t: torch.Tensor, shape, dtype, what: str, device: int):
     """(address, row stride in elements) of t [rows, cols] of a type."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{what}: {dtype} {list(shape)} on the call's device wanted")
     st = t.stride()
     if st[1] != 1 and shape[1] > 1:
@@ -672,7 +681,7 @@ def _matrix_shape(t: torch.Tensor, what: str):
 
 def _vector(t: torch.Tensor, dtype, n: int, what: str, device: int) -> int:
     """The address of a contiguous array of n elements."""
-    if t.dtype != dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous {dtype} on the call's device wanted")
     return t.data_ptr()
 
@@ -708,7 +717,7 @@ def pq_rmsnorm(x, weight, y=None, residual=None, sum=None, q=None, scale=None, r
         cp = _optional(scale, torch.float32, rows, "scale", dev)
     rc = lib.pq_rmsnorm(_dtype(x, "x"), rows, cols, xp, xs, rp, rs, sp, ss, _vector(weight, weight.dtype, cols, "weight", dev),
                         _dtype(weight, "weight"), eps, yp, ys, qp, qs, cp,
-                        _optional(rstd, torch.float32, rows, "rstd", dev), _stream(stream))
+                        _optional(rstd, torch.float32, rows, "rstd", dev), _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_rmsnorm")
 
@@ -740,7 +749,7 @@ def pq_rmsnorm_bwd(h, weight, rstd, dy, dx, dsum=None, dweight=None, workspace=N
     rc = lib.pq_rmsnorm_bwd(_dtype(h, "h"), rows, cols, hp, hs, _vector(weight, weight.dtype, cols, "weight", dev),
                             _dtype(weight, "weight"), _vector(rstd, torch.float32, rows, "rstd", dev), yp, ys, sp, ss, xp, xs,
                             _optional(dweight, torch.float32, cols, "dweight", dev), *_buffer(workspace, dev),
-                            _stream(stream))
+                            _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_rmsnorm_bwd")
 
@@ -752,7 +761,7 @@ def pq_quantize_rows(x, q, scale, stream=None) -> None:
     xp, xs = _matrix(x, shape, x.dtype, "x", dev)
     qp, qs = _matrix(q, shape, torch.int8, "q", dev)
     rc = lib.pq_quantize_rows(_dtype(x, "x"), rows, cols, xp, xs, qp, qs,
-                              _vector(scale, torch.float32, rows, "scale", dev), _stream(stream))
+                              _vector(scale, torch.float32, rows, "scale", dev), _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_quantize_rows")
 
@@ -777,22 +786,27 @@ def pq_gemm_a8(mode, x, x_scale, packed, alpha, y, bias=None, activation=PQ_ACT_
     kind, dev = y.dtype, _device(x, "x")
     xp, xs = _matrix(x, xshape, torch.int8, "x", dev)
     yp, ys = _matrix(y, (M, N), kind, "y", dev)
-    e = pq_epilogue(None, None, 0, 0, activation, combine, 0)
-    if bias is not None:
-        e.bias, e.bias_dtype = _vector(bias, bias.dtype, N, "bias", dev), _dtype(bias, "bias")
-    if other is not None:
-        e.other, e.other_stride = _matrix(other, (M, N), kind, "other", dev)
+    epilogue = None
+    if bias is not None or other is not None or activation != PQ_ACT_NONE:
+        bp = op = bd = os = 0
+        if bias is not None:
+            bp, bd = _vector(bias, bias.dtype, N, "bias", dev), _dtype(bias, "bias")
+        if other is not None:
+            op, os = _matrix(other, (M, N), kind, "other", dev)
+        epilogue = _EPILOGUE.pack(bp, op, os, bd, activation, combine, 0)
     if M == 1 and xs < K:                # the stride of a single row does not matter
         xs = K
-    if packed.dtype != torch.uint8 or packed.numel() < pq_packed_bytes(mode, N, K) or packed.get_device() != dev or \
-            not packed.is_contiguous():
+    size = (K * CODE_BITS.get(mode, 0) + 511) // 512 * ((N + 15) // 16) * 1024          # pq_packed_bytes
+    if packed.dtype is not torch.uint8 or packed.numel() < size or packed.get_device() != dev or not packed.is_contiguous():
         raise ValueError("packed: the uint8 array of pq_pack on the call's device wanted")
     if workspace is None:
-        with _memory_of(stream):
-            workspace = a8_workspace(mode, M, N, K, x.device)
+        need = lib.pq_gemm_a8_workspace_bytes(mode, M, N, K)
+        if need > 0:
+            with _memory_of(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     rc = lib.pq_gemm_a8(mode, M, N, K, xp, xs, _vector(x_scale, torch.float32, M, "x_scale", dev), packed.data_ptr(),
-                        _vector(alpha, alpha.dtype, N, "alpha", dev), _dtype(alpha, "alpha"), ctypes.addressof(e),
-                        _dtype(y, "y"), yp, ys, *_buffer(workspace, dev), _stream(stream))
+                        _vector(alpha, alpha.dtype, N, "alpha", dev), _dtype(alpha, "alpha"), epilogue,
+                        _dtype(y, "y"), yp, ys, *_buffer(workspace, dev), _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_gemm_a8")
 
@@ -817,7 +831,7 @@ def pq_distill(logits, index, top, loss=None, stats=None, dlogits=None, temperat
     rc = lib.pq_distill(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
                         _optional(row_weight, torch.float32, rows, "row_weight", dev),
                         _optional(loss, torch.float32, rows, "loss", dev), _optional(stats, torch.float32, 2 * rows, "stats", dev),
-                        grad_scale, dp, ds, _stream(stream))
+                        grad_scale, dp, ds, _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_distill")
 
@@ -830,6 +844,6 @@ def pq_distill_bwd(logits, index, top, stats, dloss, dlogits, temperature=1.0, r
     rc = lib.pq_distill_bwd(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
                             _optional(row_weight, torch.float32, rows, "row_weight", dev),
                             _vector(stats, torch.float32, 2 * rows, "stats", dev), _vector(dloss, torch.float32, rows, "dloss", dev),
-                            dp, ds, _stream(stream))
+                            dp, ds, _launch_stream(stream, dev))
     if rc:
         raise PQError(rc, "pq_distill_bwd")

@@ -107,6 +107,8 @@ def test_epilogue_refusals(pq, over, status):
 
 
 def test_gemm_workspace(pq):
+    for m, n, k in ((0, 1, 64), (4, 17, 8256), (2, 640, 192)):        # what the binding takes pq_packed_bytes to be
+        assert pq.pq_packed_bytes(m, n, k) == (k * pq.CODE_BITS[m] + 511) // 512 * ((n + 15) // 16) * 1024
     w = pq.pq_gemm_a8_workspace_bytes
     assert w(9, 1, 1, 64) == -1 and w(2, -1, 1, 64) == -1 and w(2, 1, 1, 65) == -1 and w(2, 1, 1, 1 << 17) == -1
     assert w(2, 0, 0, 64) == 0 and w(2, 1, 16, 64) % 16 == 0
@@ -178,12 +180,12 @@ def world(monkeypatch, pq):
         w.calls.append(args)
         return 0
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)        # what get_device() says of a CPU tensor
+    monkeypatch.setattr(pq, "_current_raw_stream", lambda device: 0)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
     monkeypatch.setattr(pq, "lib", types.SimpleNamespace(
         pq_rmsnorm=call, pq_rmsnorm_bwd=call, pq_quantize_rows=call, pq_gemm_a8=call, pq_distill=call, pq_distill_bwd=call,
-        pq_rmsnorm_bwd_workspace_bytes=lambda *a: 64, pq_gemm_a8_workspace_bytes=lambda *a: 64,
-        pq_packed_bytes=lambda *a: 64))
+        pq_rmsnorm_bwd_workspace_bytes=lambda *a: 64, pq_gemm_a8_workspace_bytes=lambda *a: 64))
     w.spy = lambda: monkeypatch.setattr(torch, "empty", spy)
     return w
 
@@ -192,7 +194,7 @@ def test_workspaces_come_from_the_launch_stream(world):
     pq = world.pq
     h, y = torch.zeros(4, 64), torch.zeros(4, 16)
     dw, r, x8 = torch.zeros(64), torch.zeros(4), torch.zeros(4, 64, dtype=torch.int8)
-    packed = torch.zeros(64, dtype=torch.uint8)
+    packed = torch.zeros(1024, dtype=torch.uint8)
     world.spy()
     pq.pq_rmsnorm_bwd(h, dw, r, h, torch.zeros(4, 64), dweight=dw, stream=77)
     pq.pq_gemm_a8(2, x8, r, packed, torch.zeros(16), y, stream=77)
@@ -204,11 +206,10 @@ def test_workspaces_come_from_the_launch_stream(world):
 def test_binding_refuses_other_tensors(world, monkeypatch):
     pq = world.pq
     x, w, q, s = torch.zeros(4, 64), torch.zeros(64), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
-    packed, y = torch.zeros(64, dtype=torch.uint8), torch.zeros(4, 16)
+    packed, y = torch.zeros(1024, dtype=torch.uint8), torch.zeros(4, 16)
     z, ix, t = torch.zeros(4, 50), torch.zeros(4, 3, dtype=torch.int32), torch.zeros(4, 3)
     good = [lambda: pq.pq_rmsnorm(x, w, y=torch.zeros(4, 64)), lambda: pq.pq_quantize_rows(x, q, s),
             lambda: pq.pq_gemm_a8(2, q, s, packed, torch.zeros(16), y, stream=1), lambda: pq.pq_distill(z, ix, t, s, stream=1)]
-    monkeypatch.setattr(pq, "_stream", lambda s: 0)
     for f in good:
         f()
     bad = [lambda: pq.pq_rmsnorm(x[0], w, y=x), lambda: pq.pq_rmsnorm(x, w[:63], y=x), lambda: pq.pq_rmsnorm(x, w, y=x[:3]),
@@ -217,7 +218,7 @@ def test_binding_refuses_other_tensors(world, monkeypatch):
            lambda: pq.pq_rmsnorm(x, w, y=x, residual=x.half(), sum=x), lambda: pq.pq_rmsnorm(x, w, y=x, rstd=s.double()),
            lambda: pq.pq_rmsnorm_bwd(x, w, s, x[:, :63], x), lambda: pq.pq_rmsnorm_bwd(x, w, s[:1], x, x),
            lambda: pq.pq_rmsnorm_bwd(x, w, s, x, x, dweight=s), lambda: pq.pq_quantize_rows(x, q.to(torch.uint8), s),
-           lambda: pq.pq_gemm_a8(2, x, s, packed, torch.zeros(16), y), lambda: pq.pq_gemm_a8(2, q, s, packed[:63], torch.zeros(16), y),
+           lambda: pq.pq_gemm_a8(2, x, s, packed, torch.zeros(16), y), lambda: pq.pq_gemm_a8(2, q, s, packed[:1023], torch.zeros(16), y),
            lambda: pq.pq_gemm_a8(2, q, s, packed, torch.zeros(15), y), lambda: pq.pq_gemm_a8(2, q, s, packed, torch.zeros(16), y[:3]),
            lambda: pq.pq_gemm_a8(2, q, s, packed, torch.zeros(16), y, other=y.half()),
            lambda: pq.pq_gemm_a8(2, q, s, packed, torch.zeros(16), y, bias=s),
