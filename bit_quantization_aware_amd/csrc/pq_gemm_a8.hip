@@ -95,24 +95,28 @@ __global__ __launch_bounds__(512) void k_a8_stream(A8Args a)
 // Output tiles of many rows: WN waves side by side, each 16 MT rows by 16 NT
 // columns, over K in stages of 128.  A stage's activations (128 bytes a row,
 // 16-byte chunks swizzled as in the bf16 kernels) and code bytes go from memory
-// to LDS directly, into a ring of P slots.
-template <int BITS, int WN, int MT, int NT, int P>
+// to LDS directly, into a ring of P slots.  KG groups of such waves take every
+// KG-th stage and add their sums at the end: a small tile's stage is so short
+// that the turn to the next one costs more than its products.
+template <int BITS, int WN, int KG, int MT, int NT, int P>
 struct TileCfg {
-    static constexpr int BM = 16 * MT, BN = 16 * NT * WN, THREADS = 64 * WN;
+    static constexpr int BM = 16 * MT, BN = 16 * NT * WN, THREADS = 64 * WN * KG;
     static constexpr int PIECES = BITS == 4 ? 4 : 2;            // 16-byte pieces of a column a stage (1 bit: two stages' worth)
     static constexpr int XB = BM * 128, CB = BN * PIECES * 16, SLOT = XB + CB;
     static constexpr int XI = XB / 1024 / WN, CI = CB / 1024 / WN;   // loads a wave and stage
     static constexpr int EPI = 8 * MT * (BN * 4 + 16);              // the epilogue's half tile
-    static constexpr int LDS = P * SLOT > EPI ? P * SLOT : EPI;
+    static constexpr int LDS = P * KG * SLOT > EPI ? P * KG * SLOT : EPI;
     static_assert(XI * WN * 1024 == XB && CI * WN * 1024 == CB, "whole loads");
 };
 
-template <int BITS, int WN, int MT, int NT, int P>
-__global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, int ntiles)
+template <int BITS, int WN, int KG, int MT, int NT, int P>
+__global__ __launch_bounds__(64 * WN * KG, 2) void k_a8_tile(A8Args a, int mtiles, int ntiles)
 {
-    using C = TileCfg<BITS, WN, MT, NT, P>;
+    using C = TileCfg<BITS, WN, KG, MT, NT, P>;
+    static_assert(MT < 8 || KG == 1, "the large tile has one group");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int w = KG == 1 ? wave : wave % WN, kg = KG == 1 ? 0 : wave / WN;
     const int i16 = lane & 15, g = lane >> 4;
 
     // One XCD's blocks take consecutive tiles, eight row tiles by all columns
@@ -143,17 +147,20 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     }
     const uint32_t lds_base = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds));
-    // the block's share of K: stages [first, last); the large tile takes all
+    // the block's share of K: stages [first, last); only the smallest tile's is a part
     const int stages = (a.K / 64 + 1) / 2, share = static_cast<int>(blockIdx.y);
-    const int first = MT == 8 ? 0 : share * stages / a.splits, last = MT == 8 ? stages : (share + 1) * stages / a.splits;
+    const int first = MT > 2 ? 0 : share * stages / a.splits, last = MT > 2 ? stages : (share + 1) * stages / a.splits;
     const int steps = min(a.K / 64, 2 * last) - 2 * first;
+    const int turns = (last - first + KG - 1) / KG;
 
-    // Stage s to its slot; past the last one the last again, so that the
-    // number of loads in flight is the same at every wait.  The second half of
-    // an odd last stage is not there: its chunks read the first half.
-    auto issue = [&](int s, int slot) __attribute__((always_inline)) {
-        s = min(s, last - 1);
-        const uint32_t at = lds_base + slot * C::SLOT;
+    // The group's stage of turn t to its slot; past the last one the last
+    // again, so that the number of loads in flight is the same at every wait.
+    // The second half of an odd last stage is not there: its chunks read the
+    // first half.
+    auto stage_of = [&](int t) __attribute__((always_inline)) { return first + KG * t + kg; };
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const int s = min(stage_of(t), last - 1);
+        const uint32_t at = lds_base + (slot * KG + kg) * C::SLOT;
         const uint32_t back = far & (2 * s + 1 < a.K / 64 ? 0 : 64);
 #pragma unroll
         for (int q = 0; q < C::XI; ++q) dma16(xb + s * 128, xo[q] - back, at + (C::XI * w + q) * 1024);
@@ -172,8 +179,8 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
 
     const uint8_t *xr[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) xr[h] = lds + i16 * 128 + (((4 * h + g) ^ xswz(i16)) << 4);
-    const uint8_t *cr = lds + C::XB + w * NT * (C::PIECES * 256) + i16 * 16 +
+    for (int h = 0; h < 2; ++h) xr[h] = lds + kg * C::SLOT + i16 * 128 + (((4 * h + g) ^ xswz(i16)) << 4);
+    const uint8_t *cr = lds + kg * C::SLOT + C::XB + w * NT * (C::PIECES * 256) + i16 * 16 +
                         (BITS == 4 ? (g >> 1) * 256 + (g & 1) * 8 : BITS == 2 ? g * 4 : (g >> 1) * 4);
 
     // Operands of a step of 64: activations and the code words.
@@ -183,7 +190,7 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     };
     auto read_codes = [&](auto h_c, int s, int slot, Operands &o) __attribute__((always_inline)) {
         constexpr int H = decltype(h_c)::value;
-        const uint8_t *cp = cr + slot * C::SLOT + (BITS == 4 ? H * 512 : BITS == 2 ? H * 256 : H * 8 + (s & 1) * 256);
+        const uint8_t *cp = cr + slot * (KG * C::SLOT) + (BITS == 4 ? H * 512 : BITS == 2 ? H * 256 : H * 8 + (s & 1) * 256);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if constexpr (BITS == 4) {
@@ -196,7 +203,7 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
         }
     };
     auto read_rows = [&](auto h_c, int slot, int i, Operands &o) __attribute__((always_inline)) {
-        o.x[i] = *reinterpret_cast<const intx4 *>(xr[decltype(h_c)::value] + slot * C::SLOT + i * 2048);
+        o.x[i] = *reinterpret_cast<const intx4 *>(xr[decltype(h_c)::value] + slot * (KG * C::SLOT) + i * 2048);
     };
     // The products of a step, a column tile at a time.  While one's run, the
     // next one's codes are decoded (at the end those of `then`, the first of
@@ -233,17 +240,17 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     };
 
 #pragma unroll
-    for (int s = 0; s < P; ++s) issue(first + s, s);
+    for (int t = 0; t < P; ++t) issue(t, t);
     wait_vmcnt<(P - 1) * (C::XI + C::CI)>();
     block_barrier();
     int slot = 0;
-    // Every read of the stage in `slot` is done in all waves and the next stage
-    // has landed: the slot takes stage s + P.
-    auto turn = [&](int s) __attribute__((always_inline)) {
+    // Every read of the slot's stages is done in all waves and the next turn's
+    // stages have landed: the slot takes those of turn t + P.
+    auto turn = [&](int t) __attribute__((always_inline)) {
         wait_lgkmcnt0();
         wait_vmcnt<(P - 2) * (C::XI + C::CI)>();
         block_barrier();
-        issue(s + P, slot);
+        issue(t + P, slot);
         __builtin_amdgcn_sched_barrier(0);
         slot = slot == P - 1 ? 0 : slot + 1;
     };
@@ -254,35 +261,37 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
         Operands even, odd;
         read_all(half0, first, 0, even);
         b = decode(a, even.w[0]);
-        for (int s = first; s < first + steps / 2; ++s) {
-            multiply(even, odd.w[0], half1, s, slot, odd);
-            turn(s);
-            multiply(odd, even.w[0], half0, s + 1, slot, even);
+        for (int t = 0; t < steps / 2; ++t) {
+            multiply(even, odd.w[0], half1, first + t, slot, odd);
+            turn(t);
+            multiply(odd, even.w[0], half0, first + t + 1, slot, even);
         }
         if (steps & 1) multiply(even, odd.w[0], half0, 0, slot, odd);
     } else {
         // A step's products are shorter than a read's way: operands a whole
         // stage ahead.
         Operands x0, x1, y0, y1;
-        read_all(half0, first, 0, x0);
-        read_all(half1, first, 0, x1);
+        read_all(half0, stage_of(0), 0, x0);
+        read_all(half1, stage_of(0), 0, x1);
         b = decode(a, x0.w[0]);
-        auto stage = [&](int s, Operands &c0, Operands &c1, Operands &n0, Operands &n1) __attribute__((always_inline)) {
-            turn(s);
-            multiply(c0, c1.w[0], half0, s + 1, slot, n0);
-            multiply(c1, n0.w[0], half1, s + 1, slot, n1);
+        auto stage = [&](int t, Operands &c0, Operands &c1, Operands &n0, Operands &n1) __attribute__((always_inline)) {
+            turn(t);
+            multiply(c0, c1.w[0], half0, stage_of(t + 1), slot, n0);
+            multiply(c1, n0.w[0], half1, stage_of(t + 1), slot, n1);
         };
+        // the last turn, in which a group may have no stage, or half of one
         auto end = [&](Operands &c0, Operands &c1, Operands &n0) __attribute__((always_inline)) {
-            multiply(c0, c1.w[0], half0, last - 1, slot, n0);
-            if (!(steps & 1)) multiply(c1, c1.w[0], half0, last - 1, slot, n0);
+            const int s = stage_of(turns - 1);
+            if (s < last) multiply(c0, c1.w[0], half0, s, slot, n0);
+            if (s < last && 2 * s + 1 < a.K / 64) multiply(c1, c1.w[0], half0, s, slot, n0);
         };
-        int s = first;
-        for (; s + 2 < last; s += 2) {
-            stage(s, x0, x1, y0, y1);
-            stage(s + 1, y0, y1, x0, x1);
+        int t = 0;
+        for (; t + 2 < turns; t += 2) {
+            stage(t, x0, x1, y0, y1);
+            stage(t + 1, y0, y1, x0, x1);
         }
-        if (s + 1 < last) {
-            stage(s, x0, x1, y0, y1);
+        if (t + 1 < turns) {
+            stage(t, x0, x1, y0, y1);
             end(y0, y1, x0);
         } else {
             end(x0, x1, y0);
@@ -294,15 +303,22 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
     // row tiles at a time, rows 16 bytes further apart than they are long (the
     // sixteen rows of a write then lie in different banks).  A thread takes the
     // same eight columns of every TR-th row.
-    constexpr int RS = C::BN * 4 + 16, TC = C::BN / 8, TR = C::THREADS / TC, RT = 8 * MT / TR;
+    constexpr int RS = C::BN * 4 + 16, TC = C::BN / 8, HR = 8 * MT;        // HR: rows of a half
+    constexpr int TR = C::THREADS / TC < HR ? C::THREADS / TC : HR, RT = HR / TR;
     const int tc = threadIdx.x % TC, tr = threadIdx.x / TC, c = (n0 >> 3) + tc;
     auto to_lds = [&](int half) __attribute__((always_inline)) {
-        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < MT / 2; ++i)
+        for (int k = KG - 1; k >= 0; --k) {
+            __syncthreads();
+            if (KG > 1 && kg != k) continue;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                *reinterpret_cast<intx4 *>(lds + (16 * i + i16) * RS + ((w * NT + j) * 16 + 4 * g) * 4) = acc[half * (MT / 2) + i][j];
+            for (int i = 0; i < MT / 2; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    intx4 *p = reinterpret_cast<intx4 *>(lds + (16 * i + i16) * RS + ((w * NT + j) * 16 + 4 * g) * 4);
+                    *p = k == KG - 1 ? acc[half * (MT / 2) + i][j] : acc[half * (MT / 2) + i][j] + *p;
+                }
+        }
         __syncthreads();
     };
     auto sums = [&](int r, int (&sum)[8]) __attribute__((always_inline)) {
@@ -313,13 +329,13 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
             sum[4 + e] = p[1][e];
         }
     };
-    if (MT < 8 && a.splits > 1) {   // the sums as they are, joined by k_a8_join
+    if (MT == 2 && a.splits > 1) {  // the sums as they are, joined by k_a8_join
         int32_t *out = a.partial + static_cast<int64_t>(blockIdx.y) * a.M * a.p_st;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int row0 = m0 + half * (MT / 2) * 16;
             to_lds(half);
-            for (int r = tr; r < min(8 * MT, a.M - row0); r += TR) {
+            for (int r = tr; r < min(HR, a.M - row0); r += C::THREADS / TC) {
                 const intx4 *p = reinterpret_cast<const intx4 *>(lds + r * RS + tc * 32);
                 intx4 *to = reinterpret_cast<intx4 *>(out + (row0 + r) * a.p_st + 8 * c);
                 if (8 * c < a.p_st) {
@@ -338,21 +354,22 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
         T *y = static_cast<T *>(a.Y);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int row0 = m0 + half * (MT / 2) * 16, rows = min(8 * MT, a.M - row0);
-            if (n0 + C::BN <= a.N && rows == 8 * MT) {
+            const int row0 = m0 + half * (MT / 2) * 16, rows = min(HR, a.M - row0);
+            if (n0 + C::BN <= a.N && rows == HR) {
                 // a whole half: everything that it loads is on its way while
                 // the sums go through LDS
                 Raw8<T> o[RT];
                 float rs[RT];
 #pragma unroll
                 for (int k = 0; k < RT; ++k) {
-                    const int64_t m = row0 + tr + k * TR;
+                    const int64_t m = row0 + min(tr, TR - 1) + k * TR;
                     if (other) o[k] = load_whole8(other + m * a.o_st + 8 * c);
                     rs[k] = a.x_scale[m];
                 }
                 to_lds(half);
 #pragma unroll
                 for (int k = 0; k < RT; ++k) {
+                    if (tr >= TR) break;        // a half of fewer rows than threads
                     int sum[8];
                     float v[8];
                     sums(tr + k * TR, sum);
@@ -364,7 +381,7 @@ __global__ __launch_bounds__(64 * WN, 2) void k_a8_tile(A8Args a, int mtiles, in
             } else {
                 to_lds(half);
                 if (8 * c < a.N)
-                    for (int r = tr; r < rows; r += TR) {
+                    for (int r = tr; r < rows; r += C::THREADS / TC) {
                         int sum[8];
                         sums(r, sum);
                         finish8<T>(a, row0 + r, c, a.x_scale[row0 + r], sum, cs, cb);
@@ -400,36 +417,42 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
     with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, m, c, a.x_scale[m], sum, cs, cb); });
 }
 
-// How a shape is cut: 128 x 256 tiles where they give every CU one, else 64 x
-// 128 ones (32 x 128 up to 32 rows), with K split while that gives no CU a
-// second block, eight stages a share at least (two blocks a CU: 512 rows, N =
-// K = 4096, 22.9 us against 15.8 unsplit; 64 rows, N = 4096, K = 14336, 19.6
-// against 16.9: the partial sums cost more than the second block brings).
+// How a shape is cut.  128 x 256 tiles where they give every CU one.  Else 64 x
+// 128, of one group of waves where there are two a CU and of two groups down to
+// 192 tiles (1024 rows of N = K = 4096, 512 tiles: 23 us against 26; 512 rows,
+// 256 tiles: 16 against 14; 1024 rows of 1600 x 1600, 208 tiles: 9.5 against
+// 8.7, with 32-row tiles 10.4).  Below that 32 x 128 (64 rows of 14336 x 4096 11.2
+// us, with 64-row tiles 13.5), and up to 64 such tiles K is split until there are
+// 256, eight stages a share at least: the partial sums and the second launch
+// cost 2 to 4 us (64 rows of 4096 x 14336 27 us unsplit, 19 and 15 with two and
+// four shares; 128 rows of 4096 x 4096, 128 tiles: 11.2 and 12.7 with two).
 struct A8Plan {
-    int mt, splits;          // 16-row tiles a block (0: the stream kernel), shares of K
+    int mt, groups;          // 16-row tiles a block (0: the stream kernel), groups of waves
+    int splits;              // shares of K
     int64_t p_st;            // columns of a row of partial sums
 };
 
 inline A8Plan a8_plan(int64_t M, int64_t N, int64_t K)
 {
-    if (M <= 16) return {0, 1, 0};
-    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return {8, 1, 0};
-    const int mt = M <= 32 ? 2 : 4;
-    const int64_t blocks = ((M + 16 * mt - 1) / (16 * mt)) * ((N + 127) / 128), stages = (K / 64 + 1) / 2;
-    int64_t splits = 256 / blocks;
+    if (M <= 16) return {0, 1, 1, 0};
+    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return {8, 1, 1, 0};
+    const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
+    if (M > 32 && tiles >= 192) return {4, tiles >= 512 ? 1 : 2, 1, 0};
+    const int64_t blocks = ((M + 31) / 32) * ((N + 127) / 128), stages = (K / 64 + 1) / 2;
+    int64_t splits = blocks <= 64 ? 256 / blocks : 1;
     if (splits > stages / 8) splits = stages / 8;
-    if (splits < 2) return {mt, 1, 0};
-    return {mt, static_cast<int>(splits), (N + 7) / 8 * 8};
+    if (splits < 2) return {2, 2, 1, 0};
+    return {2, 2, static_cast<int>(splits), (N + 7) / 8 * 8};
 }
 
-template <int BITS, int WN, int MT, int NT, int P>
+template <int BITS, int WN, int KG, int MT, int NT, int P>
 pq_status launch_tile(const A8Args &a, hipStream_t s)
 {
-    using C = TileCfg<BITS, WN, MT, NT, P>;
+    using C = TileCfg<BITS, WN, KG, MT, NT, P>;
     const int mtiles = (a.M + C::BM - 1) / C::BM, ntiles = (a.N + C::BN - 1) / C::BN;
     const int64_t blocks = static_cast<int64_t>(mtiles) * ntiles;
     if (blocks > kMaxBlocks) return PQ_ERR_SHAPE;
-    hipLaunchKernelGGL((k_a8_tile<BITS, WN, MT, NT, P>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.splits)),
+    hipLaunchKernelGGL((k_a8_tile<BITS, WN, KG, MT, NT, P>), dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.splits)),
                        dim3(C::THREADS), 0, s, a, mtiles, ntiles);
     if (hipGetLastError() != hipSuccess) return PQ_ERR_HIP;
     if (a.splits == 1) return PQ_OK;
@@ -453,9 +476,10 @@ pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
             hipLaunchKernelGGL((k_a8_stream<BITS, 1, U>), dim3(tiles), dim3(512), 0, s, a);
         return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
     }
-    if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 4>(a, s);
-    if (plan.mt == 4) return launch_tile<BITS, 4, 4, 2, 4>(a, s);
-    return launch_tile<BITS, 4, 8, 4, BITS == 4 ? 2 : 3>(a, s);
+    if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 2, 3>(a, s);
+    if (plan.mt == 4 && plan.groups == 2) return launch_tile<BITS, 4, 2, 4, 2, 3>(a, s);
+    if (plan.mt == 4) return launch_tile<BITS, 4, 1, 4, 2, 4>(a, s);
+    return launch_tile<BITS, 4, 1, 8, 4, BITS == 4 ? 2 : 3>(a, s);
 }
 
 inline bool a8_shape_ok(int mode, int64_t M, int64_t N, int64_t K)

@@ -81,6 +81,47 @@ def test_shapes(pq, shape, mode):
     y.check("y")
 
 
+# many tiles: 64 x 128 ones in two groups of waves and in one, 128 x 256 ones; a last stage that is whole, half, the only one
+LARGE = [(1500, 1100, 320), (1411, 1153, 64), (2100, 2100, 192), (2049, 2200, 1088), (2200, 4100, 448), (4000, 2177, 128), (2051, 4097, 1600)]
+
+
+@pytest.mark.parametrize("mode", [0, 2, 3, 4])
+@pytest.mark.parametrize("shape", LARGE)
+def test_large(pq, shape, mode):
+    print(f"[a8 large mode={mode} {shape}]", flush=True)
+    c = Case(mode, *shape)
+    y = Guarded(shape[:2], torch.bfloat16)
+    pq.pq_gemm_a8(mode, c.x, c.x_scale, c.packed, c.alpha, y.t)
+    c.check(y.t)
+    y.check("y")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(1500, 1100, 320), (2100, 2100, 192), (2200, 4100, 448), (2304, 3840, 256)])
+def test_large_epilogue(pq, shape, dtype):
+    """Every type, both combinations, rows of wider arrays; whole tiles and ragged ones."""
+    print(f"[a8 large epilogue {shape} {dtype}]", flush=True)
+    m, n, _ = shape
+    c = Case(2, *shape, seed=6)
+    bias, other = c.random(n, dtype=dtype), c.random(m, n + 3, dtype=dtype)[:, 1:1 + n]
+    y = torch.full((m, n + 5), 3.0, dtype=dtype, device=DEV)
+    for kind, mul in ((2, True), (4, False)):
+        pq.pq_gemm_a8(2, c.x, c.x_scale, c.packed, c.alpha, y[:, 2:2 + n], bias=bias, activation=kind, other=other,
+                      combine=pq.PQ_COMBINE_MUL if mul else pq.PQ_COMBINE_ADD)
+        c.check(y[:, 2:2 + n], kind, bias, other, mul)
+    assert bool((y[:, :2] == 3).all()) and bool((y[:, 2 + n:] == 3).all())
+    pq.pq_gemm_a8(2, c.x, c.x_scale, c.packed, c.alpha, other, bias=bias, activation=4, other=other)         # in place
+    assert torch.equal(other, y[:, 2:2 + n])
+
+
+def test_output_past_the_caches(pq):
+    """An output so large that it is written with streaming stores."""
+    c = Case(2, 8192, 8200, 64, seed=7)
+    y = torch.empty(8192, 8200, dtype=torch.bfloat16, device=DEV)
+    pq.pq_gemm_a8(2, c.x, c.x_scale, c.packed, c.alpha, y)
+    c.check(y)
+
+
 @pytest.mark.parametrize("mode", sorted(R.LEVELS))
 @pytest.mark.parametrize("shape", [(5, 50, 640), (150, 300, 1216), (600, 600, 1024)])
 def test_modes(pq, shape, mode):
@@ -158,7 +199,7 @@ def test_empty(pq):
     pq.pq_gemm_a8(2, c.x, c.x_scale, torch.empty(0, dtype=torch.uint8, device=DEV), torch.empty(0, device=DEV), torch.empty(1, 0, device=DEV))
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 500, 2048), (48, 96, 8192), (333, 1600, 4352), (700, 900, 512)])
+@pytest.mark.parametrize("m,n,k", [(1, 500, 2048), (48, 96, 8192), (333, 1600, 4352), (700, 900, 512), (1600, 1100, 576), (2100, 4000, 320)])
 def test_workspace_and_repeats(pq, m, n, k):
     """A workspace of any contents, larger than needed, shared by calls one after the other: the same bits every time."""
     c = Case(2, m, n, k, seed=5)
