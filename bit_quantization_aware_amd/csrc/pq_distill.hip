@@ -339,7 +339,7 @@ __global__ __launch_bounds__(512) void k_distill_bwd(DistillArgs a)
 // 2048 rows of 128256 words in bf16 93 us against 108; with the gradient 262
 // against 218.  One form for both gives one loss, bit for bit.)
 template <typename T>
-pq_status launch_distill(const DistillArgs &a, hipStream_t s)
+pq_status launch_rows(const DistillArgs &a, hipStream_t s)
 {
     const dim3 grid(static_cast<unsigned>(a.rows));
     if (a.vocab <= 256 * 8 * 4) hipLaunchKernelGGL((k_distill<T, 256, 4>), grid, dim3(256), 0, s, a);
@@ -349,6 +349,36 @@ pq_status launch_distill(const DistillArgs &a, hipStream_t s)
         hipLaunchKernelGGL((k_distill<T, 1024, sizeof(T) == 2 ? 16 : 0>), grid, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL((k_distill<T, 1024, 0>), grid, dim3(1024), 0, s, a);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
+}
+
+template <typename T>
+pq_status launch_bwd_rows(const DistillArgs &a, hipStream_t s)
+{
+    const int64_t chunks = a.vocab / 8 > 0 ? a.vocab / 8 : 1;
+    hipLaunchKernelGGL(k_distill_bwd<T>, dim3(static_cast<unsigned>(a.rows), static_cast<unsigned>((chunks + a.segment - 1) / a.segment)),
+                       dim3(512), 0, s, a);
+    return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
+}
+
+template <typename T, typename F>
+pq_status launch_distill(DistillArgs a, F &&launch)
+{
+    const int tsize = dtype_bytes(a.top_dtype);
+    for (int64_t left = a.rows; left > 0; left -= kLaunchRows) {
+        a.rows = static_cast<int>(left < kLaunchRows ? left : kLaunchRows);
+        const pq_status rc = launch(a);
+        if (rc != PQ_OK) return rc;
+        skip_rows(a.z, a.rows, a.z_st, sizeof(T));
+        skip_rows(a.dz, a.rows, a.d_st, sizeof(T));
+        skip_rows(a.index, a.rows, a.k, 4);
+        skip_rows(a.top, a.rows, a.k, tsize);
+        skip_rows(a.row_weight, a.rows, 1, 4);
+        skip_rows(a.dloss, a.rows, 1, 4);
+        skip_rows(a.stats_in, a.rows, 2, 4);
+        skip_rows(a.loss, a.rows, 1, 4);
+        skip_rows(a.stats, a.rows, 2, 4);
+    }
+    return PQ_OK;
 }
 
 inline bool misaligned(const void *p, int size) { return reinterpret_cast<uintptr_t>(p) % size != 0; }
@@ -362,7 +392,8 @@ inline pq_status distill_args(DistillArgs &a, int dtype, int64_t rows, int64_t v
     if (!size || !tsize) return PQ_ERR_MODE;
     if (rows < 0 || rows > INT32_MAX || vocab < 1 || vocab > (int64_t(1) << 30) || k < 1 || k > kMaxTop) return PQ_ERR_SHAPE;
     const float temp = static_cast<float>(temperature), inv = static_cast<float>(1.0 / temperature);
-    if (!(temperature > 0.0) || !(temp > 0.f) || !(inv > 0.f) || !std::isfinite(temp) || !std::isfinite(inv))
+    const float c = static_cast<float>(1.4426950408889634074 / temperature);
+    if (!(temperature > 0.0) || !(temp > 0.f) || !(inv > 0.f) || !std::isfinite(temp) || !std::isfinite(c))
         return PQ_ERR_ARG;
     if (rows == 0) return PQ_OK;
     if (!logits || !index || !top) return PQ_ERR_NULL;
@@ -383,7 +414,7 @@ inline pq_status distill_args(DistillArgs &a, int dtype, int64_t rows, int64_t v
     a.top_dtype = top_dtype;
     a.temp = temp;
     a.inv_temp = inv;
-    a.c = static_cast<float>(1.4426950408889634074 / temperature);
+    a.c = c;
     // Half the memory-side cache's size and more is written past the caches
     // (2048 x 128256 in bf16 208 us against 218, 512 x 200000 103 against 119);
     // less may be found there by its reader (517 x 32003 in fp32 28 against 41).
@@ -414,9 +445,11 @@ pq_status pq_distill(int dtype, int64_t rows, int64_t vocab, const void *logits,
     a.stats = stats;
     a.grad = grad_scale * temperature;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return dtype == PQ_F32    ? launch_distill<float>(a, s)
-           : dtype == PQ_BF16 ? launch_distill<bf16_t>(a, s)
-                              : launch_distill<f16_t>(a, s);
+    auto with = [&](auto type) {
+        using T = decltype(type);
+        return launch_distill<T>(a, [&](const DistillArgs &b) { return launch_rows<T>(b, s); });
+    };
+    return dtype == PQ_F32 ? with(float{}) : dtype == PQ_BF16 ? with(bf16_t{}) : with(f16_t{});
 }
 
 pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t l_stride, int64_t k,
@@ -436,17 +469,16 @@ pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *log
     a.dloss = dloss;
     a.grad = temperature;
     const int64_t chunks = vocab / 8 > 0 ? vocab / 8 : 1;
-    // up to 65535 blocks a row, of 4096 words and more
+    // up to 65535 blocks a row, of 32768 words and more
     int64_t segments = (chunks + 4095) / 4096;
     if (segments > 65535) segments = 65535;
     a.segment = static_cast<int>((chunks + segments - 1) / segments);
-    segments = (chunks + a.segment - 1) / a.segment;
-    const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(segments));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == PQ_F32) hipLaunchKernelGGL(k_distill_bwd<float>, grid, dim3(512), 0, s, a);
-    else if (dtype == PQ_BF16) hipLaunchKernelGGL(k_distill_bwd<bf16_t>, grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL(k_distill_bwd<f16_t>, grid, dim3(512), 0, s, a);
-    return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
+    auto with = [&](auto type) {
+        using T = decltype(type);
+        return launch_distill<T>(a, [&](const DistillArgs &b) { return launch_bwd_rows<T>(b, s); });
+    };
+    return dtype == PQ_F32 ? with(float{}) : dtype == PQ_BF16 ? with(bf16_t{}) : with(f16_t{});
 }
 
 }  // extern "C"

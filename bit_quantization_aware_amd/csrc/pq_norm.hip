@@ -318,7 +318,7 @@ pq_status with_shape(int64_t cols, F &&f)
 inline unsigned team_blocks(int64_t rows, int team) { return static_cast<unsigned>(team == 64 ? (rows + 3) / 4 : rows); }
 
 template <typename T, bool NORM>
-pq_status launch_norm(const NormArgs &a, hipStream_t s)
+pq_status launch_rows(const NormArgs &a, hipStream_t s)
 {
     return with_shape(a.cols, [&](auto team, auto nv) {
         constexpr int TEAM = decltype(team)::value, NV = decltype(nv)::value;
@@ -336,6 +336,24 @@ pq_status launch_norm(const NormArgs &a, hipStream_t s)
             return PQ_ERR_SHAPE;
         }
     });
+}
+
+template <typename T, bool NORM>
+pq_status launch_norm(NormArgs a, hipStream_t s)
+{
+    for (int64_t left = a.rows; left > 0; left -= kLaunchRows) {
+        a.rows = left < kLaunchRows ? left : kLaunchRows;
+        const pq_status rc = launch_rows<T, NORM>(a, s);
+        if (rc != PQ_OK) return rc;
+        skip_rows(a.x, a.rows, a.x_st, sizeof(T));
+        skip_rows(a.residual, a.rows, a.r_st, sizeof(T));
+        skip_rows(a.sum, a.rows, a.s_st, sizeof(T));
+        skip_rows(a.y, a.rows, a.y_st, sizeof(T));
+        skip_rows(a.q, a.rows, a.q_st, 1);
+        skip_rows(a.scale, a.rows, 1, 4);
+        skip_rows(a.rstd, a.rows, 1, 4);
+    }
+    return PQ_OK;
 }
 
 // Blocks of the gradient, each with a row of partial sums: two of 256 threads a

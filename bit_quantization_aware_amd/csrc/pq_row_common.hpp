@@ -93,6 +93,17 @@ __device__ __forceinline__ void store_row8(T *row, int c, int cols, const float 
         if (8 * c + e < cols) p[e] = from_f32<T>(x[e]);
 }
 
+// Rows of one launch, a block of up to 1024 threads each: a grid's threads are
+// counted in 32 bits.  More rows go in several launches.
+constexpr int64_t kLaunchRows = int64_t(1) << 21;
+
+// Moves a pointer that may be NULL by `rows` rows of `stride` elements.
+template <typename P>
+inline void skip_rows(P *&p, int64_t rows, int64_t stride, int size)
+{
+    if (p) p = reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(rows * stride * size));
+}
+
 // Eight values of an array of any element type (a run-time choice that is the
 // same for all threads).
 __device__ __forceinline__ void load_any8(const void *a, int dtype, int c, int cols, float (&x)[8])

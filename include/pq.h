@@ -745,7 +745,8 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
  * output in 8 bits on request:
  *   h = x + residual (rounded to the type; x itself without a residual)
  *   y = h rstd weight,   rstd = (mean_j h_j^2 + eps)^(-1/2)
- * in fp32, y rounded once -- to the type, or to 8 bits as above.
+ * in fp32 (a row whose squares add up to 2^128 and more has rstd 0), y rounded
+ * once -- to the type, or to 8 bits as above.
  *   dtype      of x, residual, sum and y: PQ_F32, PQ_BF16 or PQ_F16
  *   rows       at most 2^31 - 1;  cols 1 .. 32768
  *   residual   in [rows, cols], or NULL;  sum out h, required with it (NULL
@@ -815,7 +816,8 @@ typedef struct pq_epilogue {
  * is an integer sum on the matrix unit and exact; what follows is fp32,
  * rounded once to y's type.
  *   mode       a deployable width
- *   M, N       0 .. 2^24;  K a positive multiple of 64, at most 2^17 - 64
+ *   M, N       0 .. 2^24, up to 2^24 - 1 tiles of 128 x 256 (else
+ *              PQ_ERR_SHAPE);  K a positive multiple of 64, at most 2^17 - 64
  *              (the sums then fit 32 bits)
  *   X          in [M, K] int8 codes, 16-byte aligned, x_stride a multiple of 16,
  *              K .. 2^23
@@ -844,8 +846,9 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
  *   loss[r] = row_weight[r] T^2 sum_j p_j (ln p_j - ln q_index[j])
  *   dlogits[r, i] = grad_scale row_weight[r] T (q_i - p_i)
  * i.e. the gradient of grad_scale * sum_r loss[r], computed while the row is
- * at hand.  A row of weight 0 or without a valid entry has loss 0 and gradient
- * 0, whatever its logits hold; an entry of p_j = 0 adds nothing to the loss.
+ * at hand.  A row of weight 0, or without an entry that counts and is above
+ * -inf, has loss 0 and gradient 0, whatever its logits hold (and stats (0, 1));
+ * an entry of p_j = 0 adds nothing to the loss.
  * A logit of -inf has q_i = 0; NaN, +inf and rows of nothing but -inf give NaN.
  *   dtype       of logits and dlogits
  *   rows        at most 2^31 - 1;  vocab 1 .. 2^30;  k 1 .. 1024

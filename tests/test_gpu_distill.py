@@ -164,3 +164,31 @@ def test_gradient_against_differences(pq):
     slope = (f(z + e * d) - f(z - e * d)) / (2 * e)
     # third derivative of T^2 log-sum-exp(z / T) along d: at most max|d|^3 / T; a loss of up to 100 is rounded to 2^-18
     assert float((slope - (dz.double() * d.double()).sum(-1)).abs().max()) < e * e * 4.5 ** 3 / 2 / 6 * 4 + 2.0 ** -17 / e
+
+
+def test_more_rows_than_a_launch(pq):
+    """Rows past 2^21, which go in a second launch."""
+    rows, v, k = (1 << 21) + 3, 17, 2
+    z = torch.randn(rows, v, device=DEV).to(torch.bfloat16)
+    index = (torch.arange(rows, device=DEV, dtype=torch.int32)[:, None] * 3 + torch.tensor([0, 5], dtype=torch.int32, device=DEV)) % v
+    top, weight = torch.randn(rows, k, device=DEV), (torch.rand(rows, device=DEV) < 0.9).float()
+    loss, stats, dz = torch.empty(rows, device=DEV), torch.empty(rows, 2, device=DEV), torch.empty_like(z)
+    pq.pq_distill(z, index, top, loss, stats, dz, row_weight=weight)
+    check(z, index, top, 1.0, weight, loss, dz, 1.0)
+    dz2 = torch.empty_like(z)
+    pq.pq_distill_bwd(z, index, top, stats, torch.ones(rows, device=DEV), dz2, row_weight=weight)
+    check(z, index, top, 1.0, weight, None, dz2, 1.0)
+
+
+@pytest.mark.parametrize("fill", [float("-inf"), 0.0])
+def test_lists_filled_up_with_one_word(pq, fill):
+    """A list of 1024 entries that is one word for the most part, with and without weight: the sum over it is exact."""
+    rows, v = 3, 5000
+    z, index, top = make(rows, v, 1024, torch.float32, 11)
+    index[:, 20:], top[:, 20:] = 7, fill
+    loss, dz = torch.empty(rows, device=DEV), torch.empty_like(z)
+    pq.pq_distill(z, index, top, loss, dlogits=dz)
+    check(z, index, top, 1.0, None, loss, dz, 1.0)
+    again = torch.empty_like(dz)
+    pq.pq_distill(z, index, top, dlogits=again)
+    assert torch.equal(again, dz)

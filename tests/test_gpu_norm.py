@@ -196,3 +196,25 @@ def test_gradient_against_differences(pq):
     want = (dx.double() * d.double()).sum() + (dw.double() * v.double()).sum()
     # third derivative: e^2 / 6 of terms of size |dy| |d|^3; rounding: 2^-23 |y| |dy| / e, both over 20480 values in quadrature
     assert abs(float(slope - want)) < 20480 ** 0.5 * (e * e * 4 + 2.0 ** -22 * 3 / e)
+
+
+def test_more_rows_than_a_launch(pq):
+    """Rows past 2^21, which go in a second launch."""
+    rows, cols = (1 << 21) + 5, 8
+    x = torch.randn(rows, cols, device=DEV, dtype=torch.float32).to(torch.bfloat16)
+    w, q, scale, rstd = torch.ones(cols, device=DEV), torch.empty(rows, cols, dtype=torch.int8, device=DEV), \
+        torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    s = torch.empty_like(x)
+    pq.pq_rmsnorm(x, w, residual=x, sum=s, q=q, scale=scale, rstd=rstd)
+    assert torch.equal(s, x + x)
+    check_rows(q, scale, R.norm(s, w, 1e-6)[0], FP32)
+    want = R.norm(s, w, 1e-6)[1]
+    within(rstd, want, FP32 * want, "rstd")
+    pq.pq_quantize_rows(x, q, scale)
+    check_rows(q, scale, x.double(), 0.0)
+    dx, dw = torch.empty_like(x), torch.empty(cols, device=DEV)
+    pq.pq_rmsnorm_bwd(x, w, rstd, s, dx, dweight=dw)
+    dxw, dww, size, dsize = R.norm_grad(x, w, rstd, s)
+    within(dx, dxw, R.U[x.dtype] * dxw.abs() + 2.0 ** -24 * 86 * size + R.TINY[x.dtype], "dx")
+    # 512 rows one after the other in each of 4096 waves, then 16 and 64 sums
+    within(dw, dww, 2.0 ** -24 * (512 + 96) * dsize, "dweight")

@@ -95,6 +95,15 @@ def test_gemm_refusals(pq, at, value, status):
     assert pq.lib.pq_gemm_a8(*a) == status
 
 
+def test_gemm_refuses_more_tiles_than_a_launch(pq):
+    a = gemm_args(pq)
+    a[1] = a[2] = a[13] = 1 << 24
+    assert pq.lib.pq_gemm_a8(*a) == 2
+    a = gemm_args(pq)
+    a[5] = (1 << 23) + 16
+    assert pq.lib.pq_gemm_a8(*a) == 2
+
+
 @pytest.mark.parametrize("over,status", [
     ({"activation": 5}, 3), ({"activation": -1}, 3), ({"combine": 2}, 3), ({"bias": A, "bias_dtype": 3}, 3),
     ({"bias": A + 2, "bias_dtype": 0}, 4), ({"other": C + 1}, 4), ({"other": C, "other_stride": 64}, 7), ({"reserved": 1}, 7)])
