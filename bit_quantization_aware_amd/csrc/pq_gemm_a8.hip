@@ -18,78 +18,129 @@ constexpr int64_t kMaxA8K = (int64_t(1) << 17) - 64;
 constexpr int64_t kMaxA8 = int64_t(1) << 24;
 constexpr int64_t kMaxXStride = int64_t(1) << 23;    // a tile's rows are within 32 bits of its first
 
-// Up to 16 rows: the weights' stream bounds it, so a block takes NT 16-column
-// tiles, its eight waves every eighth 64-byte group of K, and the code bytes go
-// to registers with the streaming hint (they are read once).  No activations
-// in LDS: a lane reads the sixteen values that its codes stand against.  The
-// loads of U groups, and what the epilogue reads, are in flight before the
-// first is used.
-template <int BITS, int NT, int U>
-__global__ __launch_bounds__(512) void k_a8_stream(A8Args a)
+// Up to 16 rows: the weights' stream bounds it, and memory gives its rate only
+// with tens of KB in flight a CU.  A block takes TN 16-column tiles; its NW waves
+// share K by 64-byte groups of codes, wave w taking groups w, w + NW, ..., each
+// through a ring of D stages in LDS of its own that direct loads fill (codes with
+// the streaming hint: they are read once), so that a wave waits for its own loads
+// only and the block meets once, to add the sums.  In the export byte order the
+// blocks of a launch then read one window of consecutive addresses.
+// A load of activations brings RPL rows' chunks of a group, interleaved by 16
+// bytes, and lies 16 RPL bytes further from the next than it is long, so that
+// sixteen rows' reads fall on different banks; rows past M read the last one.
+// 16384 x 16384 at 2 bits, out of HBM: 14.9 us with one row, 16.5 with sixteen
+// (4.5 and 4.1 TB/s; codes and activations loaded to registers 20 and 28, the
+// activations' 16-byte pieces of many rows being what that waits for).
+template <int BITS, int TN, int XI>
+struct StreamShape {
+    static constexpr int GK = 512 / BITS, STEPS = GK / 64;      // k and products of a group
+    static constexpr int RPL = 1024 / GK, XS = 1024 + 16 * RPL; // rows a load, bytes between loads
+    // eight waves' rings of sixteen 1-bit rows (8 KB a stage) do not fit
+    static constexpr int NW = BITS == 1 && XI == 8 ? 4 : 8, D = 2, SLOT = TN * 1024 + XI * XS;
+    static constexpr int RED = NW * TN * 16 * 80;               // the waves' sums: rows of 16 tiles' columns, 16 bytes apart
+    static constexpr int LDS = NW * D * SLOT > RED ? NW * D * SLOT : RED;
+};
+
+template <int BITS, int TN, int XI>
+__global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI>::NW)) void k_a8_stream(A8Args a)
 {
-    constexpr int GK = 512 / BITS, STEPS = GK / 64;             // k and products of a group
-    __shared__ intx4 red[8][NT][16 * 5];        // a wave's sums: rows of 16, 16 bytes apart
+    using C = StreamShape<BITS, TN, XI>;
+    constexpr int GK = C::GK, RPL = C::RPL, NW = C::NW, D = C::D;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int i16 = lane & 15, g = lane >> 4;
-    const int groups = (a.K + GK - 1) / GK, last_tile = (a.N - 1) >> 4;
-    // the epilogue's share of a lane: eight columns of a row, in the last waves
-    const int to = static_cast<int>(threadIdx.x) - (512 - 32 * NT), r = (to >> 1) & 15, tile = to >> 5, h = to & 1;
-    const int c = (blockIdx.x * NT + tile) * 2 + h;
-    const bool writes = to >= 0 && r < a.M && 8 * c < a.N;
-    float cs[8], cb[8], rs = 0.f;
-    if (writes) {
-        columns8(a, c, cs, cb);
-        rs = a.x_scale[r];
-    }
-    intx4 acc[NT];
+    const int groups = (a.K + GK - 1) / GK, turns = groups > w ? (groups - w + NW - 1) / NW : 0;
+    const int last_tile = (a.N - 1) >> 4;
+    uint32_t co[TN], xo[XI];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = intx4{0, 0, 0, 0};
-    const int8_t *x = a.X + min(i16, a.M - 1) * a.x_st;
-    const uint8_t *codes[NT];
+    for (int t = 0; t < TN; ++t)
+        co[t] = static_cast<uint32_t>(min(static_cast<int>(blockIdx.x) * TN + t, last_tile) * 1024 + i16 * 64 + g * 16);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        codes[t] = a.packed + static_cast<int64_t>(min(static_cast<int>(blockIdx.x) * NT + t, last_tile)) * 1024 + i16 * 64 + g * 16;
-    for (int q0 = w; q0 < groups; q0 += 8 * U) {
-        u32x4 cw[U][NT];
-        intx4 v[U][STEPS];
+    for (int q = 0; q < XI; ++q) xo[q] = static_cast<uint32_t>(min(RPL * q + lane % RPL, a.M - 1) * a.x_st);
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds)) +
+                          w * (D * C::SLOT);
+    auto issue = [&](int t, int slot) __attribute__((always_inline)) {
+        const int group = w + NW * t;
+        const uint8_t *cb = a.packed + group * a.gstride;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int i = 0; i < TN; ++i) dma16<true>(cb, co[i], ring + slot * C::SLOT + i * 1024);
+        // chunks past K: the row's last one (no product is made of them)
+        const uint32_t k = static_cast<uint32_t>(min(group * GK + lane / RPL * 16, a.K - 16));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                cw[u][t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(codes[t] + min(q0 + 8 * u, groups - 1) * a.gstride));
+        for (int q = 0; q < XI; ++q) dma16(a.X, xo[q] + k, ring + slot * C::SLOT + TN * 1024 + q * C::XS);
+    };
+    intx4 acc[TN];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+    for (int t = 0; t < TN; ++t) acc[t] = intx4{0, 0, 0, 0};
+    const int row = min(i16, a.M - 1);
+    const uint8_t *own = lds + w * (D * C::SLOT);
+    const uint8_t *xr = own + TN * 1024 + row / RPL * C::XS + row % RPL * 16 + g * (C::STEPS * 16 * RPL);
+    auto compute = [&](int t, int slot) __attribute__((always_inline)) {
+        u32x4 c[TN];
+        intx4 x[C::STEPS];
 #pragma unroll
-            for (int j = 0; j < STEPS; ++j) {
-                const int k = (q0 + 8 * u) * GK + g * (GK / 4) + j * 16;      // past K: no product
-                v[u][j] = intx4{0, 0, 0, 0};
-                if (k < a.K) v[u][j] = *reinterpret_cast<const intx4 *>(x + k);
+        for (int i = 0; i < TN; ++i) c[i] = *reinterpret_cast<const u32x4 *>(own + slot * C::SLOT + i * 1024 + lane * 16);
+#pragma unroll
+        for (int j = 0; j < C::STEPS; ++j) x[j] = *reinterpret_cast<const intx4 *>(xr + slot * C::SLOT + j * (16 * RPL));
+        const int k = (w + NW * t) * GK + g * (GK / 4);
+        if ((w + NW * t + 1) * GK > a.K) {
+#pragma unroll
+            for (int j = 0; j < C::STEPS; ++j)
+                if (k + 16 * j >= a.K) x[j] = intx4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < C::STEPS; ++j)
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                Words<BITS> wd;
+                if constexpr (BITS == 1) wd.w = c[i][j >> 1] >> (16 * (j & 1));
+                if constexpr (BITS == 2) wd.w = c[i][j];
+                if constexpr (BITS == 4) wd = {c[i][2 * j], c[i][2 * j + 1]};
+                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode(a, wd), x[j], acc[i], 0, 0, 0);
             }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < STEPS; ++j)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    Words<BITS> wd;
-                    if constexpr (BITS == 1) wd.w = cw[u][t][j >> 1] >> (16 * (j & 1));
-                    if constexpr (BITS == 2) wd.w = cw[u][t][j];
-                    if constexpr (BITS == 4) wd = {cw[u][t][2 * j], cw[u][t][2 * j + 1]};
-                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode(a, wd), v[u][j], acc[t], 0, 0, 0);
-                }
+    };
+    for (int t = 0; t < min(D, turns); ++t) issue(t, t);
+    int t = 0, slot = 0;
+    for (; t + D < turns; ++t) {
+        wait_vmcnt<(D - 1) * (TN + XI)>();
+        compute(t, slot);
+        wait_lgkmcnt0();                // the slot's reads have returned
+        issue(t + D, slot);
+        slot = slot + 1 == D ? 0 : slot + 1;
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) red[w][t][i16 * 5 + g] = acc[t];
+    static_for<0, D>([&](auto left) {
+        constexpr int after = D - 1 - decltype(left)::value;    // turns issued after this one
+        const int at = turns - 1 - after;
+        if (at >= t) {
+            wait_vmcnt<after * (TN + XI)>();
+            compute(at, at % D);
+        }
+    });
     __syncthreads();
-    if (!writes) return;
-    int sum[8];
+    intx4 *red = reinterpret_cast<intx4 *>(lds);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0;
+    for (int i = 0; i < TN; ++i) red[(w * TN + i) * 80 + i16 * 5 + g] = acc[i];
+    __syncthreads();
+    // a lane takes eight columns of a row
+    for (int at = threadIdx.x; at < 32 * TN; at += 64 * NW) {
+        const int h = at % (2 * TN), r = at / (2 * TN), c = blockIdx.x * (2 * TN) + h;
+        if (r >= a.M || 8 * c >= a.N) continue;
+        intx4 lo = {0, 0, 0, 0}, hi = lo;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < NW; ++i) {
+            lo += red[(i * TN + (h >> 1)) * 80 + r * 5 + 2 * (h & 1)];
+            hi += red[(i * TN + (h >> 1)) * 80 + r * 5 + 2 * (h & 1) + 1];
+        }
+        int sum[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += red[i][tile][r * 5 + 2 * h + (e >> 2)][e & 3];
-    with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, r, c, rs, sum, cs, cb); });
+        for (int e = 0; e < 4; ++e) {
+            sum[e] = lo[e];
+            sum[4 + e] = hi[e];
+        }
+        float cs[8], cb[8];
+        columns8(a, c, cs, cb);
+        with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, r, c, a.x_scale[r], sum, cs, cb); });
+    }
 }
 
 // Output tiles of many rows: WN waves side by side, each 16 MT rows by 16 NT
@@ -461,20 +512,36 @@ pq_status launch_tile(const A8Args &a, hipStream_t s)
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
+template <int BITS, int XI, int TN>
+pq_status launch_stream_tn(const A8Args &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_a8_stream<BITS, TN, XI>), dim3(static_cast<unsigned>((a.N + 16 * TN - 1) / (16 * TN))), dim3(64 * StreamShape<BITS, TN, XI>::NW), 0, s, a);
+    return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
+}
+
+// Column tiles a block: four or two while that leaves over 192 blocks (16 rows
+// of 14336 columns, K = 4096: 224 blocks of four 6.8 us, 448 of two 10.0: the
+// activations are read once a block).
+template <int BITS, int XI>
+pq_status launch_stream(const A8Args &a, hipStream_t s)
+{
+    if (a.N > 16 * 4 * 192) return launch_stream_tn<BITS, XI, 4>(a, s);
+    if (a.N > 16 * 2 * 192) return launch_stream_tn<BITS, XI, 2>(a, s);
+    return launch_stream_tn<BITS, XI, 1>(a, s);
+}
+
 template <int BITS>
 pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
 {
     if (plan.mt == 0) {
-        const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
-        constexpr int U = BITS == 1 ? 1 : 2;
-        // Two column tiles a block halve the reads of the activations, where
-        // they are several rows and there is a block for every CU all the same
-        // (16 rows, N = 14336, K = 4096: 7.8 us against 10.8).
-        if (a.M > 4 && tiles >= 512)
-            hipLaunchKernelGGL((k_a8_stream<BITS, 2, U>), dim3((tiles + 1) / 2), dim3(512), 0, s, a);
-        else
-            hipLaunchKernelGGL((k_a8_stream<BITS, 1, U>), dim3(tiles), dim3(512), 0, s, a);
-        return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
+        constexpr int RPL = 1024 / (512 / BITS);
+        const int xi = (a.M + RPL - 1) / RPL;           // loads of activations a group
+        if (xi == 1) return launch_stream<BITS, 1>(a, s);
+        if (xi == 2) return launch_stream<BITS, 2>(a, s);
+        if constexpr (RPL <= 4) {
+            if (xi <= 4) return launch_stream<BITS, 4>(a, s);
+        }
+        if constexpr (RPL <= 2) return launch_stream<BITS, 8>(a, s);
     }
     if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 2, 3>(a, s);
     if (plan.mt == 4 && plan.groups == 2) return launch_tile<BITS, 4, 2, 4, 2, 3>(a, s);

@@ -788,25 +788,29 @@ def pq_gemm_a8(mode, x, x_scale, packed, alpha, y, bias=None, activation=PQ_ACT_
     yp, ys = _matrix(y, (M, N), kind, "y", dev)
     epilogue = None
     if bias is not None or other is not None or activation != PQ_ACT_NONE:
-        bp = op = bd = os = 0
+        bp = op = bd = ot = 0
         if bias is not None:
             bp, bd = _vector(bias, bias.dtype, N, "bias", dev), _dtype(bias, "bias")
         if other is not None:
-            op, os = _matrix(other, (M, N), kind, "other", dev)
-        epilogue = _EPILOGUE.pack(bp, op, os, bd, activation, combine, 0)
-    if M == 1 and xs < K:                # the stride of a single row does not matter
+            op, ot = _matrix(other, (M, N), kind, "other", dev)
+        epilogue = _EPILOGUE.pack(bp, op, ot, bd, activation, combine, 0)
+    if M == 1:                           # the stride of a single row does not matter
         xs = K
     size = (K * CODE_BITS.get(mode, 0) + 511) // 512 * ((N + 15) // 16) * 1024          # pq_packed_bytes
     if packed.dtype is not torch.uint8 or packed.numel() < size or packed.get_device() != dev or not packed.is_contiguous():
         raise ValueError("packed: the uint8 array of pq_pack on the call's device wanted")
-    if workspace is None:
+    xsp, ap, ad, yd = _vector(x_scale, torch.float32, M, "x_scale", dev), _vector(alpha, alpha.dtype, N, "alpha", dev), \
+        _dtype(alpha, "alpha"), _dtype(y, "y")
+    launch = _launch_stream(stream, dev)
+    wp, wb = _buffer(workspace, dev)
+    rc = lib.pq_gemm_a8(mode, M, N, K, xp, xs, xsp, packed.data_ptr(), ap, ad, epilogue, yd, yp, ys, wp, wb, launch)
+    if rc == 1 and workspace is None:    # the shape needs a workspace; most do not, so nobody is asked beforehand
         need = lib.pq_gemm_a8_workspace_bytes(mode, M, N, K)
         if need > 0:
             with _memory_of(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    rc = lib.pq_gemm_a8(mode, M, N, K, xp, xs, _vector(x_scale, torch.float32, M, "x_scale", dev), packed.data_ptr(),
-                        _vector(alpha, alpha.dtype, N, "alpha", dev), _dtype(alpha, "alpha"), epilogue,
-                        _dtype(y, "y"), yp, ys, *_buffer(workspace, dev), _launch_stream(stream, dev))
+            rc = lib.pq_gemm_a8(mode, M, N, K, xp, xs, xsp, packed.data_ptr(), ap, ad, epilogue, yd, yp, ys,
+                                workspace.data_ptr(), need, launch)
     if rc:
         raise PQError(rc, "pq_gemm_a8")
 

@@ -188,12 +188,15 @@ def world(monkeypatch, pq):
     def call(*args):
         w.calls.append(args)
         return 0
+    def gemm(*args):
+        w.calls.append(args)
+        return 1 if args[-3] is None else 0         # a shape that needs a workspace
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)        # what get_device() says of a CPU tensor
     monkeypatch.setattr(pq, "_current_raw_stream", lambda device: 0)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
     monkeypatch.setattr(pq, "lib", types.SimpleNamespace(
-        pq_rmsnorm=call, pq_rmsnorm_bwd=call, pq_quantize_rows=call, pq_gemm_a8=call, pq_distill=call, pq_distill_bwd=call,
+        pq_rmsnorm=call, pq_rmsnorm_bwd=call, pq_quantize_rows=call, pq_gemm_a8=gemm, pq_distill=call, pq_distill_bwd=call,
         pq_rmsnorm_bwd_workspace_bytes=lambda *a: 64, pq_gemm_a8_workspace_bytes=lambda *a: 64))
     w.spy = lambda: monkeypatch.setattr(torch, "empty", spy)
     return w
@@ -207,7 +210,8 @@ def test_workspaces_come_from_the_launch_stream(world):
     world.spy()
     pq.pq_rmsnorm_bwd(h, dw, r, h, torch.zeros(4, 64), dweight=dw, stream=77)
     pq.pq_gemm_a8(2, x8, r, packed, torch.zeros(16), y, stream=77)
-    assert world.made == [("external", 77)] * 2 and [c[-1] for c in world.calls] == [77, 77]
+    assert world.made == [("external", 77)] * 2 and [c[-1] for c in world.calls] == [77, 77, 77]
+    assert [c[-2] for c in world.calls] == [64, 0, 64]      # the product is tried without one first
     pq.pq_gemm_a8(2, x8, r, packed, torch.zeros(16), y, stream=77, workspace=torch.zeros(64, dtype=torch.uint8))
     assert len(world.made) == 2
 
