@@ -468,15 +468,16 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
     with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, m, c, a.x_scale[m], sum, cs, cb); });
 }
 
-// How a shape is cut.  128 x 256 tiles where they give every CU one.  Else 64 x
-// 128, of one group of waves where there are two a CU and of two groups down to
-// 192 tiles (1024 rows of N = K = 4096, 512 tiles: 23 us against 26; 512 rows,
-// 256 tiles: 16 against 14; 1024 rows of 1600 x 1600, 208 tiles: 9.5 against
-// 8.7, with 32-row tiles 10.4).  Below that 32 x 128 (64 rows of 14336 x 4096 11.2
-// us, with 64-row tiles 13.5), and up to 64 such tiles K is split until there are
-// 256, eight stages a share at least: the partial sums and the second launch
-// cost 2 to 4 us (64 rows of 4096 x 14336 27 us unsplit, 19 and 15 with two and
-// four shares; 128 rows of 4096 x 4096, 128 tiles: 11.2 and 12.7 with two).
+// How a shape is cut.  128 x 256 tiles from 176 of them on (512 rows of 14336 x
+// 4096, 224 tiles: 33 us against 40; 333 rows, 168 tiles: 34 both ways; 256 rows,
+// 112 tiles: 31 against 21).  Else 64 x 128, of one group of waves
+// where there are two a CU and of two groups down to 192 tiles (1024 rows of N =
+// K = 4096, 512 tiles: 23 us against 26; 512 rows, 256 tiles: 16 against 14; 1024
+// rows of 1600 x 1600, 208 tiles: 9.5 against 8.7, with 32-row tiles 10.4).  Below
+// that 32 x 128 (64 rows of 14336 x 4096 11.2 us, with 64-row tiles 13.5), with K
+// split while that pays: a stage takes 0.19 us, a second launch and the way of
+// the partial sums 3 us and their 8 bytes at 4 TB/s (64 rows of 4096 x 14336 27 us
+// in one share, 19 and 15 in two and four; 128 rows of 4096 x 4096 11.2 and 12.7).
 struct A8Plan {
     int mt, groups;          // 16-row tiles a block (0: the stream kernel), groups of waves
     int splits;              // shares of K
@@ -486,12 +487,19 @@ struct A8Plan {
 inline A8Plan a8_plan(int64_t M, int64_t N, int64_t K)
 {
     if (M <= 16) return {0, 1, 1, 0};
-    if (((M + 127) / 128) * ((N + 255) / 256) >= 256) return {8, 1, 1, 0};
+    if (((M + 127) / 128) * ((N + 255) / 256) >= 176) return {8, 1, 1, 0};
     const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
     if (M > 32 && tiles >= 192) return {4, tiles >= 512 ? 1 : 2, 1, 0};
     const int64_t blocks = ((M + 31) / 32) * ((N + 127) / 128), stages = (K / 64 + 1) / 2;
-    int64_t splits = blocks <= 64 ? 256 / blocks : 1;
-    if (splits > stages / 8) splits = stages / 8;
+    int64_t splits = 1;
+    double least = 190.0 * stages;                      // ns
+    for (int64_t n = 2; n * blocks <= 256 && 4 * n <= stages; ++n) {
+        const double cost = 190.0 * ((stages + n - 1) / n) + 3000.0 + 0.002 * M * N * n;
+        if (cost < least) {
+            least = cost;
+            splits = n;
+        }
+    }
     if (splits < 2) return {2, 2, 1, 0};
     return {2, 2, static_cast<int>(splits), (N + 7) / 8 * 8};
 }

@@ -666,10 +666,10 @@ def _matrix(t: torch.Tensor, shape, dtype, what: str, device: int):
     """(address, row stride in elements) of t [rows, cols] of a type."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         raise ValueError(f"{what}: {dtype} {list(shape)} on the call's device wanted")
-    st = t.stride()
-    if st[1] != 1 and shape[1] > 1:
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
         raise ValueError(f"{what}: a contiguous last dimension wanted")
-    return t.data_ptr(), st[0]
+    return t.data_ptr(), rows
 
 
 def _matrix_shape(t: torch.Tensor, what: str):
