@@ -8,7 +8,8 @@
 // sums exp against the maximum of its own words and the (maximum, sum) pairs
 // are joined once, so there is one reduction a row; rows of up to 131072 words
 // of 16 bits (65536 of fp32) stay in registers between the sum and the
-// gradient, longer ones are read a second time.  One wave reads the teacher's
+// gradient, what longer ones have more is read a second time (1024 rows of 128256
+// words in fp32 239 us; 293 with all of it read twice).  One wave reads the teacher's
 // list while the others read the row.
 // 2048 rows of 128256 words in bf16 take 208 us, 5.06 TB/s, the rate of a copy;
 // the gradient by itself 206.
@@ -176,8 +177,8 @@ __device__ __forceinline__ void zero_words(T *dz, int from, int to, int step, in
     if (rest >= 0 && rest < vocab) dz[rest] = from_f32<T>(0.f);
 }
 
-// NV > 0: the row in registers, NV chunks a thread; NV = 0: read twice.  The
-// words behind the last whole chunk go to the first threads, one each.
+// NV chunks a thread in registers; the words behind the last whole chunk go to
+// the first threads, one each.
 template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM) void k_distill(DistillArgs a)
 {
@@ -187,61 +188,56 @@ __global__ __launch_bounds__(TEAM) void k_distill(DistillArgs a)
     const T *z = static_cast<const T *>(a.z) + r * a.z_st;
     T *dz = a.dz ? static_cast<T *>(a.dz) + r * a.d_st : nullptr;
     const float weight = a.row_weight ? a.row_weight[r] : 1.f;
-    Raw8<T> raw[NV > 0 ? NV : 1];
+    Raw8<T> raw[NV];
     float z_rest = -INFINITY;
     if (weight != 0.f) {
-        if constexpr (NV > 0) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (tid + v * TEAM < chunks) raw[v] = load_whole8(z + 8 * static_cast<int64_t>(tid + v * TEAM));
-        }
+        for (int v = 0; v < NV; ++v)
+            if (tid + v * TEAM < chunks) raw[v] = load_whole8(z + 8 * static_cast<int64_t>(tid + v * TEAM));
         if (rest < a.vocab) z_rest = to_f32(z[rest]);
     }
     if (tid < 64 && weight != 0.f) read_entries<T>(a, r, z, a.loss != nullptr, dz != nullptr, l);
     float m = z_rest, s = 0.f;
     if (weight != 0.f) {
-        if constexpr (NV > 0) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (tid + v * TEAM >= chunks) continue;
-                float x[8];
-                as_read(raw[v]);
-                raw_to_f32<T>(raw[v], x);
+        for (int v = 0; v < NV; ++v) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (tid + v * TEAM >= chunks) continue;
+            float x[8];
+            as_read(raw[v]);
+            raw_to_f32<T>(raw[v], x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, x[e]);
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, x[e]);
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (tid + v * TEAM >= chunks) continue;
-                float x[8];
-                as_read(raw[v]);
-                raw_to_f32<T>(raw[v], x);
+        for (int v = 0; v < NV; ++v) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (tid + v * TEAM >= chunks) continue;
+            float x[8];
+            as_read(raw[v]);
+            raw_to_f32<T>(raw[v], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
+        }
+        s += __builtin_amdgcn_exp2f((z_rest - ref) * a.c);
+        // what the registers do not hold
+        for (int c = tid + NV * TEAM; c < chunks; c += U * TEAM) {
+            Raw8<T> q[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c + u * TEAM >= chunks) break;
+                float x[8], more = m;
+                raw_to_f32<T>(q[u], x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) more = fmaxf(more, x[e]);
+                const float ref = more == -INFINITY ? 0.f : more;
+                s *= __builtin_amdgcn_exp2f((m - ref) * a.c);
+                m = more;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
-            }
-            s += __builtin_amdgcn_exp2f((z_rest - ref) * a.c);
-        } else {
-            s = z_rest == -INFINITY ? 0.f : 1.f;
-            for (int c = tid; c < chunks; c += U * TEAM) {
-                Raw8<T> q[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (c + u * TEAM >= chunks) break;
-                    float x[8], more = m;
-                    raw_to_f32<T>(q[u], x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) more = fmaxf(more, x[e]);
-                    const float ref = more == -INFINITY ? 0.f : more;
-                    s *= __builtin_amdgcn_exp2f((m - ref) * a.c);
-                    m = more;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s += __builtin_amdgcn_exp2f((x[e] - ref) * a.c);
-                }
             }
         }
     }
@@ -280,23 +276,20 @@ __global__ __launch_bounds__(TEAM) void k_distill(DistillArgs a)
     if (!dz) return;
     const double g = a.grad * weight;
     const float gq = static_cast<float>(g / static_cast<double>(sum)), gp = static_cast<float>(g / t_sum);
-    if constexpr (NV > 0) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (tid + v * TEAM >= chunks) continue;
-            as_read(raw[v]);
-            grad8<T>(a, l, dz, tid + v * TEAM, raw[v], top, gq, gp);
-        }
-    } else {
-        for (int c = tid; c < chunks; c += U * TEAM) {
-            Raw8<T> q[U];
+    for (int v = 0; v < NV; ++v) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (tid + v * TEAM >= chunks) continue;
+        as_read(raw[v]);
+        grad8<T>(a, l, dz, tid + v * TEAM, raw[v], top, gq, gp);
+    }
+    for (int c = tid + NV * TEAM; c < chunks; c += U * TEAM) {
+        Raw8<T> q[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
+        for (int u = 0; u < U; ++u) q[u] = load_whole8(z + 8 * static_cast<int64_t>(min(c + u * TEAM, chunks - 1)));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c + u * TEAM < chunks) grad8<T>(a, l, dz, c + u * TEAM, q[u], top, gq, gp);
-        }
+        for (int u = 0; u < U; ++u)
+            if (c + u * TEAM < chunks) grad8<T>(a, l, dz, c + u * TEAM, q[u], top, gq, gp);
     }
     if (rest < a.vocab) grad1<T>(a, l, dz, rest, z_rest, top, gq, gp);
 }
@@ -334,20 +327,18 @@ __global__ __launch_bounds__(512) void k_distill_bwd(DistillArgs a)
     if (rest >= 0 && rest < a.vocab) grad1<T>(a, l, dz, rest, to_f32(z[rest]), top, gq, gp);
 }
 
-// A row stays in registers where it fits.  (For the loss alone rows over 65536
-// words would be read faster twice over, with two blocks a CU in place of one:
-// 2048 rows of 128256 words in bf16 93 us against 108; with the gradient 262
-// against 218.  One form for both gives one loss, bit for bit.)
+// Threads and chunks by the row.  (For the loss alone rows over 65536 words would
+// be read faster past the registers, with two blocks a CU in place of one: 2048
+// rows of 128256 words in bf16 93 us against 108; with the gradient 262 against
+// 218.  One form for both gives one loss, bit for bit.)
 template <typename T>
 pq_status launch_rows(const DistillArgs &a, hipStream_t s)
 {
     const dim3 grid(static_cast<unsigned>(a.rows));
     if (a.vocab <= 256 * 8 * 4) hipLaunchKernelGGL((k_distill<T, 256, 4>), grid, dim3(256), 0, s, a);
     else if (a.vocab <= 512 * 8 * 8) hipLaunchKernelGGL((k_distill<T, 512, 8>), grid, dim3(512), 0, s, a);
-    else if (a.vocab <= 1024 * 8 * 8) hipLaunchKernelGGL((k_distill<T, 1024, 8>), grid, dim3(1024), 0, s, a);
-    else if (sizeof(T) == 2 && a.vocab <= 1024 * 8 * 16)
-        hipLaunchKernelGGL((k_distill<T, 1024, sizeof(T) == 2 ? 16 : 0>), grid, dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL((k_distill<T, 1024, 0>), grid, dim3(1024), 0, s, a);
+    else if (sizeof(T) == 4 || a.vocab <= 1024 * 8 * 8) hipLaunchKernelGGL((k_distill<T, 1024, 8>), grid, dim3(1024), 0, s, a);
+    else hipLaunchKernelGGL((k_distill<T, 1024, sizeof(T) == 2 ? 16 : 8>), grid, dim3(1024), 0, s, a);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
