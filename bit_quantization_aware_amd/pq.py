@@ -647,12 +647,23 @@ PQ_COMBINE_ADD, PQ_COMBINE_MUL = 0, 1
 _EPILOGUE = struct.Struct("PPqiiii")         # pq_epilogue; packed, it costs a call a quarter of what its fields do
 
 
-def _device(t: torch.Tensor, what: str) -> int:
-    """The current device, which all of a call's tensors have to be on."""
+# torch.cuda.current_device() without its look for an initialised runtime, which
+# a tensor on a GPU means.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _first(t: torch.Tensor, what: str):
+    """(address, row stride, shape, device) of a call's first matrix."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: [rows, cols] wanted")
     d = t.get_device()
-    if d != torch.cuda.current_device():
+    if d < 0 or d != _current_device():
         raise ValueError(f"{what}: a tensor on the current GPU wanted")
-    return d
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: a contiguous last dimension wanted")
+    return t.data_ptr(), rows, shape, d
 
 
 def _launch_stream(stream, device: int) -> Optional[int]:
@@ -670,13 +681,6 @@ def _matrix(t: torch.Tensor, shape, dtype, what: str, device: int):
     if cols != 1 and shape[1] > 1:
         raise ValueError(f"{what}: a contiguous last dimension wanted")
     return t.data_ptr(), rows
-
-
-def _matrix_shape(t: torch.Tensor, what: str):
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{what}: [rows, cols] wanted")
-    return shape
 
 
 def _vector(t: torch.Tensor, dtype, n: int, what: str, device: int) -> int:
@@ -701,9 +705,9 @@ def _buffer(t, device: int):
 
 def pq_rmsnorm(x, weight, y=None, residual=None, sum=None, q=None, scale=None, rstd=None, eps=1e-6, stream=None) -> None:
     """Norm of x (+ residual, stored in sum) [rows, cols] into y, or into int8 rows q with their scales."""
-    rows, cols = shape = _matrix_shape(x, "x")
-    kind, dev = x.dtype, _device(x, "x")
-    xp, xs = _matrix(x, shape, kind, "x", dev)
+    xp, xs, shape, dev = _first(x, "x")
+    rows, cols = shape
+    kind = x.dtype
     rp = sp = yp = qp = cp = None
     rs = ss = ys = qs = 0
     if residual is not None:
@@ -737,9 +741,9 @@ def rmsnorm_bwd_workspace(rows: int, cols: int, device="cuda") -> torch.Tensor:
 def pq_rmsnorm_bwd(h, weight, rstd, dy, dx, dsum=None, dweight=None, workspace=None, stream=None) -> None:
     """Gradient of pq_rmsnorm from what it normalised (h) and its rstd; dsum is the gradient that reaches h from
     elsewhere.  Without a workspace one is allocated for dweight."""
-    rows, cols = shape = _matrix_shape(h, "h")
-    kind, dev = h.dtype, _device(h, "h")
-    hp, hs = _matrix(h, shape, kind, "h", dev)
+    hp, hs, shape, dev = _first(h, "h")
+    rows, cols = shape
+    kind = h.dtype
     yp, ys = _matrix(dy, shape, kind, "dy", dev)
     xp, xs = _matrix(dx, shape, kind, "dx", dev)
     sp, ss = (None, 0) if dsum is None else _matrix(dsum, shape, kind, "dsum", dev)
@@ -756,9 +760,8 @@ def pq_rmsnorm_bwd(h, weight, rstd, dy, dx, dsum=None, dweight=None, workspace=N
 
 def pq_quantize_rows(x, q, scale, stream=None) -> None:
     """x [rows, cols] as int8 rows q with their scales."""
-    rows, cols = shape = _matrix_shape(x, "x")
-    dev = _device(x, "x")
-    xp, xs = _matrix(x, shape, x.dtype, "x", dev)
+    xp, xs, shape, dev = _first(x, "x")
+    rows, cols = shape
     qp, qs = _matrix(q, shape, torch.int8, "q", dev)
     rc = lib.pq_quantize_rows(_dtype(x, "x"), rows, cols, xp, xs, qp, qs,
                               _vector(scale, torch.float32, rows, "scale", dev), _launch_stream(stream, dev))
@@ -781,18 +784,21 @@ def a8_workspace(mode: int, M: int, N: int, K: int, device="cuda") -> Optional[t
 def pq_gemm_a8(mode, x, x_scale, packed, alpha, y, bias=None, activation=PQ_ACT_NONE, other=None, combine=PQ_COMBINE_ADD,
                workspace=None, stream=None) -> None:
     """y [M, N] = act(x_scale alpha (x @ levels^T) + bias) (+ or *) other, of int8 rows x [M, K] and packed weights."""
-    M, K = xshape = _matrix_shape(x, "x")
-    N = y.shape[1] if y.dim() == 2 else -1
-    kind, dev = y.dtype, _device(x, "x")
-    xp, xs = _matrix(x, xshape, torch.int8, "x", dev)
-    yp, ys = _matrix(y, (M, N), kind, "y", dev)
+    xp, xs, (M, K), dev = _first(x, "x")
+    if x.dtype is not torch.int8:
+        raise ValueError("x: int8 wanted")
+    yshape, kind = y.shape, y.dtype
+    if len(yshape) != 2 or yshape[0] != M:
+        raise ValueError("y: [rows of x, columns] wanted")
+    N = yshape[1]
+    yp, ys = _matrix(y, yshape, kind, "y", dev)
     epilogue = None
     if bias is not None or other is not None or activation != PQ_ACT_NONE:
         bp = op = bd = ot = 0
         if bias is not None:
             bp, bd = _vector(bias, bias.dtype, N, "bias", dev), _dtype(bias, "bias")
         if other is not None:
-            op, ot = _matrix(other, (M, N), kind, "other", dev)
+            op, ot = _matrix(other, yshape, kind, "other", dev)
         epilogue = _EPILOGUE.pack(bp, op, ot, bd, activation, combine, 0)
     if M == 1:                           # the stride of a single row does not matter
         xs = K
@@ -816,12 +822,12 @@ def pq_gemm_a8(mode, x, x_scale, packed, alpha, y, bias=None, activation=PQ_ACT_
 
 
 def _teacher(logits, index, top):
-    rows, vocab = shape = _matrix_shape(logits, "logits")
-    dev = _device(logits, "logits")
+    lp, ls, shape, dev = _first(logits, "logits")
+    rows, vocab = shape
     n = index.shape
     if len(n) != 2 or n[0] != rows or top.shape != n:
         raise ValueError("index, top: [rows, k] wanted")
-    return rows, vocab, shape, dev, n[1], _vector(index, torch.int32, rows * n[1], "index", dev), \
+    return lp, ls, rows, vocab, shape, dev, n[1], _vector(index, torch.int32, rows * n[1], "index", dev), \
         _vector(top, top.dtype, rows * n[1], "top", dev), _dtype(top, "top")
 
 
@@ -829,8 +835,7 @@ def pq_distill(logits, index, top, loss=None, stats=None, dlogits=None, temperat
                stream=None) -> None:
     """Loss of logits [rows, vocab] against a teacher's top logits at index [rows, k], with what pq_distill_bwd takes
     (stats [rows, 2]) and the gradient of grad_scale * loss.sum() on request."""
-    rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
-    lp, ls = _matrix(logits, shape, logits.dtype, "logits", dev)
+    lp, ls, rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
     dp, ds = (None, 0) if dlogits is None else _matrix(dlogits, shape, logits.dtype, "dlogits", dev)
     rc = lib.pq_distill(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
                         _optional(row_weight, torch.float32, rows, "row_weight", dev),
@@ -842,8 +847,7 @@ def pq_distill(logits, index, top, loss=None, stats=None, dlogits=None, temperat
 
 def pq_distill_bwd(logits, index, top, stats, dloss, dlogits, temperature=1.0, row_weight=None, stream=None) -> None:
     """Gradient of pq_distill's loss, weighed by dloss [rows], into dlogits (which may be logits)."""
-    rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
-    lp, ls = _matrix(logits, shape, logits.dtype, "logits", dev)
+    lp, ls, rows, vocab, shape, dev, k, ip, tp, td = _teacher(logits, index, top)
     dp, ds = _matrix(dlogits, shape, logits.dtype, "dlogits", dev)
     rc = lib.pq_distill_bwd(_dtype(logits, "logits"), rows, vocab, lp, ls, k, ip, tp, td, temperature,
                             _optional(row_weight, torch.float32, rows, "row_weight", dev),

@@ -191,7 +191,8 @@ def world(monkeypatch, pq):
     def gemm(*args):
         w.calls.append(args)
         return 1 if args[-3] is None else 0         # a shape that needs a workspace
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)        # what get_device() says of a CPU tensor
+    monkeypatch.setattr(pq, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
     monkeypatch.setattr(pq, "_current_raw_stream", lambda device: 0)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: ("external", handle))
@@ -250,10 +251,17 @@ def test_binding_refuses_other_tensors(world, monkeypatch):
 
 def test_binding_refuses_tensors_of_another_device(world, monkeypatch):
     pq = world.pq
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pq, "_current_device", lambda: 1)
     x, w = torch.zeros(4, 64), torch.zeros(64)
     for f in (lambda: pq.pq_rmsnorm(x, w, y=x), lambda: pq.pq_quantize_rows(x, x.to(torch.int8), torch.zeros(4)),
               lambda: pq.pq_distill(x, torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, 1), torch.zeros(4))):
         with pytest.raises(ValueError, match="current GPU"):
             f()
+    monkeypatch.setattr(pq, "_current_device", lambda: 0)
+    for where in (-1, 1):                       # the others: host memory, another GPU
+        other, out = torch.zeros(4, 64), torch.zeros(64)
+        monkeypatch.setattr(torch.Tensor, "get_device", lambda t: where if t is other or t is out else 0)
+        for f in (lambda: pq.pq_rmsnorm(x, w, y=other), lambda: pq.pq_rmsnorm(x, out, y=x), lambda: pq.pq_rmsnorm(other, w, y=x)):
+            with pytest.raises(ValueError, match="device|GPU"):
+                f()
     assert not world.calls
