@@ -18,7 +18,11 @@ constexpr int64_t kMaxA8K = (int64_t(1) << 17) - 64;
 constexpr int64_t kMaxA8 = int64_t(1) << 24;
 constexpr int64_t kMaxXStride = int64_t(1) << 23;    // a tile's rows are within 32 bits of its first
 
-// Up to 16 rows: the weights' stream bounds it, and memory gives its rate only
+// More columns than this: two column tiles a block of the stream kernel, four from
+// twice as many on.
+constexpr int64_t kStreamPair = 16 * 2 * 192;
+
+// Few rows (16 MT): the weights' stream bounds it, and memory gives its rate only
 // with tens of KB in flight a CU.  A block takes TN 16-column tiles; its NW waves
 // share K by 64-byte groups of codes, wave w taking groups w, w + NW, ..., each
 // through a ring of D stages in LDS of its own that direct loads fill (codes with
@@ -31,20 +35,20 @@ constexpr int64_t kMaxXStride = int64_t(1) << 23;    // a tile's rows are within
 // 16384 x 16384 at 2 bits, out of HBM: 14.9 us with one row, 16.5 with sixteen
 // (4.5 and 4.1 TB/s; codes and activations loaded to registers 20 and 28, the
 // activations' 16-byte pieces of many rows being what that waits for).
-template <int BITS, int TN, int XI>
+template <int BITS, int TN, int XI, int MT>
 struct StreamShape {
     static constexpr int GK = 512 / BITS, STEPS = GK / 64;      // k and products of a group
     static constexpr int RPL = 1024 / GK, XS = 1024 + 16 * RPL; // rows a load, bytes between loads
-    // eight waves' rings of sixteen 1-bit rows (8 KB a stage) do not fit
-    static constexpr int NW = BITS == 1 && XI == 8 ? 4 : 8, D = 2, SLOT = TN * 1024 + XI * XS;
-    static constexpr int RED = NW * TN * 16 * 80;               // the waves' sums: rows of 16 tiles' columns, 16 bytes apart
+    // eight waves' rings of 8 KB of activations a stage do not fit
+    static constexpr int NW = XI == 8 || MT == 2 ? 4 : 8, D = 2, SLOT = TN * 1024 + XI * XS;
+    static constexpr int RED = NW * TN * MT * 16 * 80;               // the waves' sums: rows of 16 tiles' columns, 16 bytes apart
     static constexpr int LDS = NW * D * SLOT > RED ? NW * D * SLOT : RED;
 };
 
-template <int BITS, int TN, int XI>
-__global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI>::NW)) void k_a8_stream(A8Args a)
+template <int BITS, int TN, int XI, int MT>
+__global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI, MT>::NW)) void k_a8_stream(A8Args a)
 {
-    using C = StreamShape<BITS, TN, XI>;
+    using C = StreamShape<BITS, TN, XI, MT>;
     constexpr int GK = C::GK, RPL = C::RPL, NW = C::NW, D = C::D;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -69,24 +73,35 @@ __global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI>::NW)) void k_a8_str
 #pragma unroll
         for (int q = 0; q < XI; ++q) dma16(a.X, xo[q] + k, ring + slot * C::SLOT + TN * 1024 + q * C::XS);
     };
-    intx4 acc[TN];
+    intx4 acc[MT][TN];
 #pragma unroll
-    for (int t = 0; t < TN; ++t) acc[t] = intx4{0, 0, 0, 0};
-    const int row = min(i16, a.M - 1);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[m][t] = intx4{0, 0, 0, 0};
     const uint8_t *own = lds + w * (D * C::SLOT);
-    const uint8_t *xr = own + TN * 1024 + row / RPL * C::XS + row % RPL * 16 + g * (C::STEPS * 16 * RPL);
+    const uint8_t *xr[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int row = min(16 * m + i16, a.M - 1);
+        xr[m] = own + TN * 1024 + row / RPL * C::XS + row % RPL * 16 + g * (C::STEPS * 16 * RPL);
+    }
     auto compute = [&](int t, int slot) __attribute__((always_inline)) {
         u32x4 c[TN];
-        intx4 x[C::STEPS];
+        intx4 x[MT][C::STEPS];
 #pragma unroll
         for (int i = 0; i < TN; ++i) c[i] = *reinterpret_cast<const u32x4 *>(own + slot * C::SLOT + i * 1024 + lane * 16);
 #pragma unroll
-        for (int j = 0; j < C::STEPS; ++j) x[j] = *reinterpret_cast<const intx4 *>(xr + slot * C::SLOT + j * (16 * RPL));
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < C::STEPS; ++j) x[m][j] = *reinterpret_cast<const intx4 *>(xr[m] + slot * C::SLOT + j * (16 * RPL));
         const int k = (w + NW * t) * GK + g * (GK / 4);
         if ((w + NW * t + 1) * GK > a.K) {
 #pragma unroll
             for (int j = 0; j < C::STEPS; ++j)
-                if (k + 16 * j >= a.K) x[j] = intx4{0, 0, 0, 0};
+                if (k + 16 * j >= a.K) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) x[m][j] = intx4{0, 0, 0, 0};
+                }
         }
 #pragma unroll
         for (int j = 0; j < C::STEPS; ++j)
@@ -96,7 +111,9 @@ __global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI>::NW)) void k_a8_str
                 if constexpr (BITS == 1) wd.w = c[i][j >> 1] >> (16 * (j & 1));
                 if constexpr (BITS == 2) wd.w = c[i][j];
                 if constexpr (BITS == 4) wd = {c[i][2 * j], c[i][2 * j + 1]};
-                acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(decode(a, wd), x[j], acc[i], 0, 0, 0);
+                const intx4 b = decode(a, wd);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[m][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, x[m][j], acc[m][i], 0, 0, 0);
             }
     };
     for (int t = 0; t < min(D, turns); ++t) issue(t, t);
@@ -119,17 +136,20 @@ __global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI>::NW)) void k_a8_str
     __syncthreads();
     intx4 *red = reinterpret_cast<intx4 *>(lds);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) red[(w * TN + i) * 80 + i16 * 5 + g] = acc[i];
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < TN; ++i) red[((w * MT + m) * TN + i) * 80 + i16 * 5 + g] = acc[m][i];
     __syncthreads();
     // a lane takes eight columns of a row
-    for (int at = threadIdx.x; at < 32 * TN; at += 64 * NW) {
+    for (int at = threadIdx.x; at < 32 * TN * MT; at += 64 * NW) {
         const int h = at % (2 * TN), r = at / (2 * TN), c = blockIdx.x * (2 * TN) + h;
         if (r >= a.M || 8 * c >= a.N) continue;
         intx4 lo = {0, 0, 0, 0}, hi = lo;
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
-            lo += red[(i * TN + (h >> 1)) * 80 + r * 5 + 2 * (h & 1)];
-            hi += red[(i * TN + (h >> 1)) * 80 + r * 5 + 2 * (h & 1) + 1];
+            const intx4 *p = red + ((i * MT + (r >> 4)) * TN + (h >> 1)) * 80 + (r & 15) * 5 + 2 * (h & 1);
+            lo += p[0];
+            hi += p[1];
         }
         int sum[8];
 #pragma unroll
@@ -468,7 +488,11 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
     with_type(a.y_dtype, [&](auto type) __attribute__((always_inline)) { finish8<decltype(type)>(a, m, c, a.x_scale[m], sum, cs, cb); });
 }
 
-// How a shape is cut.  128 x 256 tiles from 176 of them on (512 rows of 14336 x
+// How a shape is cut.  Up to 16 rows the stream kernel; up to 32 too (at 2 and 4
+// bits: 32 rows of 14336 x 4096 9.0 us, of 1600 x 4352 7.3, in tiles 11.8 and 9.8),
+// but for long K under few columns, where every one-tile block reads all
+// activations (32 rows of a 4-bit 4096 x 14336 16.8 us, in tiles 15.0).
+// 128 x 256 tiles from 176 of them on (512 rows of 14336 x
 // 4096, 224 tiles: 33 us against 40; 333 rows, 168 tiles: 34 both ways; 256 rows,
 // 112 tiles: 31 against 21).  Else 64 x 128, of one group of waves
 // where there are two a CU and of two groups down to 192 tiles (1024 rows of N =
@@ -484,9 +508,9 @@ struct A8Plan {
     int64_t p_st;            // columns of a row of partial sums
 };
 
-inline A8Plan a8_plan(int64_t M, int64_t N, int64_t K)
+inline A8Plan a8_plan(int bits, int64_t M, int64_t N, int64_t K)
 {
-    if (M <= 16) return {0, 1, 1, 0};
+    if (M <= 16 || (M <= 32 && bits > 1 && (N > kStreamPair || K <= 8192))) return {0, 1, 1, 0};
     if (((M + 127) / 128) * ((N + 255) / 256) >= 176) return {8, 1, 1, 0};
     const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
     if (M > 32 && tiles >= 192) return {4, tiles >= 512 ? 1 : 2, 1, 0};
@@ -520,22 +544,23 @@ pq_status launch_tile(const A8Args &a, hipStream_t s)
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
-template <int BITS, int XI, int TN>
+template <int BITS, int XI, int MT, int TN>
 pq_status launch_stream_tn(const A8Args &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_a8_stream<BITS, TN, XI>), dim3(static_cast<unsigned>((a.N + 16 * TN - 1) / (16 * TN))), dim3(64 * StreamShape<BITS, TN, XI>::NW), 0, s, a);
+    constexpr int threads = 64 * StreamShape<BITS, TN, XI, MT>::NW;
+    hipLaunchKernelGGL((k_a8_stream<BITS, TN, XI, MT>), dim3(static_cast<unsigned>((a.N + 16 * TN - 1) / (16 * TN))), dim3(threads), 0, s, a);
     return hipGetLastError() == hipSuccess ? PQ_OK : PQ_ERR_HIP;
 }
 
 // Column tiles a block: four or two while that leaves over 192 blocks (16 rows
 // of 14336 columns, K = 4096: 224 blocks of four 6.8 us, 448 of two 10.0: the
 // activations are read once a block).
-template <int BITS, int XI>
+template <int BITS, int XI, int MT = 1>
 pq_status launch_stream(const A8Args &a, hipStream_t s)
 {
-    if (a.N > 16 * 4 * 192) return launch_stream_tn<BITS, XI, 4>(a, s);
-    if (a.N > 16 * 2 * 192) return launch_stream_tn<BITS, XI, 2>(a, s);
-    return launch_stream_tn<BITS, XI, 1>(a, s);
+    if (a.N > 2 * kStreamPair) return launch_stream_tn<BITS, XI, MT, 4>(a, s);
+    if (a.N > kStreamPair) return launch_stream_tn<BITS, XI, MT, 2>(a, s);
+    return launch_stream_tn<BITS, XI, MT, 1>(a, s);
 }
 
 template <int BITS>
@@ -550,6 +575,7 @@ pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
             if (xi <= 4) return launch_stream<BITS, 4>(a, s);
         }
         if constexpr (RPL <= 2) return launch_stream<BITS, 8>(a, s);
+        if constexpr (RPL > 2) return launch_stream<BITS, 32 / RPL, 2>(a, s);
     }
     if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 2, 3>(a, s);
     if (plan.mt == 4 && plan.groups == 2) return launch_tile<BITS, 4, 2, 4, 2, 3>(a, s);
@@ -598,7 +624,7 @@ int64_t pq_gemm_a8_workspace_bytes(int mode, int64_t M, int64_t N, int64_t K)
 {
     if (!pq::a8_shape_ok(mode, M, N, K)) return -1;
     if (M == 0 || N == 0) return 0;
-    const pq::A8Plan p = pq::a8_plan(M, N, K);
+    const pq::A8Plan p = pq::a8_plan(pq::code_bits(mode), M, N, K);
     return p.splits > 1 ? p.splits * M * p.p_st * 4 : 0;
 }
 
@@ -648,7 +674,7 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
     a.act = e.activation;
     a.mul = e.other && e.combine == PQ_COMBINE_MUL;
     set_levels(a, mode);
-    const A8Plan plan = a8_plan(M, N, K);
+    const A8Plan plan = a8_plan(code_bits(mode), M, N, K);
     a.splits = plan.splits;
     a.p_st = plan.p_st;
     // An output of half the memory-side cache's size and more is not written

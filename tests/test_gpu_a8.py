@@ -67,7 +67,9 @@ def test_packing(mode):
 # one row to many, ragged columns, K that ends inside a 64-byte group of each width, sizes on both sides of the tiles
 SHAPES = [(1, 1, 64), (1, 16, 128), (2, 17, 192), (7, 40, 576), (15, 33, 320), (16, 64, 1024), (17, 48, 256), (31, 100, 704), (33, 64, 64),
           (63, 129, 448), (64, 256, 1536), (65, 300, 512), (100, 576, 960), (128, 128, 2048), (129, 257, 384), (200, 513, 640),
-          (257, 255, 1088), (300, 1000, 128), (513, 520, 832), (1, 1030, 4352), (9, 2000, 8192), (40, 31, 8256), (1025, 272, 576)]
+          (257, 255, 1088), (300, 1000, 128), (513, 520, 832), (1, 1030, 4352), (9, 2000, 8192), (40, 31, 8256), (1025, 272, 576),
+          # few rows over one, two and four column tiles a block; 17 to 32 rows on both sides of the stream kernel's limits
+          (1, 13000, 64), (5, 6300, 640), (16, 12500, 192), (20, 6200, 320), (32, 12400, 576), (18, 90, 8192), (18, 90, 8256)]
 
 
 @pytest.mark.parametrize("mode", [0, 2, 3, 4])
