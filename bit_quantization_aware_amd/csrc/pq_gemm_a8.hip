@@ -116,6 +116,8 @@ __global__ __launch_bounds__((64 * StreamShape<BITS, TN, XI, MT>::NW)) void k_a8
                 for (int m = 0; m < MT; ++m) acc[m][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b, x[m][j], acc[m][i], 0, 0, 0);
             }
     };
+    // The counted waits hold because the loop has no other vector memory operation
+    // (a spilled register would be one: every variant keeps all of its own).
     for (int t = 0; t < min(D, turns); ++t) issue(t, t);
     int t = 0, slot = 0;
     for (; t + D < turns; ++t) {
@@ -310,6 +312,7 @@ __global__ __launch_bounds__(64 * WN * KG, 2) void k_a8_tile(A8Args a, int mtile
         for (int i = 0; i < MT; ++i) read_rows(h_c, slot, i, o);
     };
 
+    // Counted waits, as in the stream kernel: nothing but `issue` touches vector memory.
 #pragma unroll
     for (int t = 0; t < P; ++t) issue(t, t);
     wait_vmcnt<(P - 1) * (C::XI + C::CI)>();
@@ -497,11 +500,13 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
 // 112 tiles: 31 against 21).  Else 64 x 128, of one group of waves
 // where there are two a CU and of two groups down to 192 tiles (1024 rows of N =
 // K = 4096, 512 tiles: 23 us against 26; 512 rows, 256 tiles: 16 against 14; 1024
-// rows of 1600 x 1600, 208 tiles: 9.5 against 8.7, with 32-row tiles 10.4).  Below
-// that 32 x 128 (64 rows of 14336 x 4096 11.2 us, with 64-row tiles 13.5), with K
-// split while that pays: a stage takes 0.19 us, a second launch and the way of
-// the partial sums 3 us and their 8 bytes at 4 TB/s (64 rows of 4096 x 14336 27 us
-// in one share, 19 and 15 in two and four; 128 rows of 4096 x 4096 11.2 and 12.7).
+// rows of 1600 x 1600, 208 tiles: 9.5 against 8.7).  Below
+// that 32 x 64, two waves and two groups, two blocks a CU (64 rows of N = K = 4096
+// 8.4 us, 128 rows with 4 bits 8.6, 200 rows of 1600 x 4352 8.9, 40 of 576 x 576
+// 4.7; as 32 x 128, one a CU, 10.5, 10.9, 11.2 and 5.5), with K split while that
+// pays: a stage takes 0.13 us, a second launch and the way of the partial sums
+// 3 us and their 8 bytes at 4 TB/s (64 rows of 4096 x 14336 27 us in one share,
+// 14.5 in four).
 struct A8Plan {
     int mt, groups;          // 16-row tiles a block (0: the stream kernel), groups of waves
     int splits;              // shares of K
@@ -514,11 +519,11 @@ inline A8Plan a8_plan(int bits, int64_t M, int64_t N, int64_t K)
     if (((M + 127) / 128) * ((N + 255) / 256) >= 176) return {8, 1, 1, 0};
     const int64_t tiles = ((M + 63) / 64) * ((N + 127) / 128);
     if (M > 32 && tiles >= 192) return {4, tiles >= 512 ? 1 : 2, 1, 0};
-    const int64_t blocks = ((M + 31) / 32) * ((N + 127) / 128), stages = (K / 64 + 1) / 2;
+    const int64_t blocks = ((M + 31) / 32) * ((N + 63) / 64), stages = (K / 64 + 1) / 2;
     int64_t splits = 1;
-    double least = 190.0 * stages;                      // ns
-    for (int64_t n = 2; n * blocks <= 256 && 4 * n <= stages; ++n) {
-        const double cost = 190.0 * ((stages + n - 1) / n) + 3000.0 + 0.002 * M * N * n;
+    double least = 125.0 * stages;                      // ns
+    for (int64_t n = 2; n * blocks <= 512 && 4 * n <= stages; ++n) {
+        const double cost = 125.0 * ((stages + n - 1) / n) + 3000.0 + 0.002 * M * N * n;
         if (cost < least) {
             least = cost;
             splits = n;
@@ -577,7 +582,7 @@ pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
         if constexpr (RPL <= 2) return launch_stream<BITS, 8>(a, s);
         if constexpr (RPL > 2) return launch_stream<BITS, 32 / RPL, 2>(a, s);
     }
-    if (plan.mt == 2) return launch_tile<BITS, 4, 2, 2, 2, 3>(a, s);
+    if (plan.mt == 2) return launch_tile<BITS, 2, 2, 2, 2, 4>(a, s);
     if (plan.mt == 4 && plan.groups == 2) return launch_tile<BITS, 4, 2, 4, 2, 3>(a, s);
     if (plan.mt == 4) return launch_tile<BITS, 4, 1, 4, 2, 4>(a, s);
     return launch_tile<BITS, 4, 1, 8, 4, BITS == 4 ? 2 : 3>(a, s);

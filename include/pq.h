@@ -830,6 +830,8 @@ typedef struct pq_epilogue {
  *   workspace  device memory of pq_gemm_a8_workspace_bytes(mode, M, N, K)
  *              bytes, 16-byte aligned (NULL where that is 0); its contents on
  *              entry do not matter.  Calls that overlap need different ones
+ * Caches: with M <= 32 the codes may be read with the streaming hint, as in
+ * pq_gemm's weight streaming; larger M reads them with ordinary loads.
  */
 int64_t pq_gemm_a8_workspace_bytes(int mode, int64_t M, int64_t N, int64_t K);
 pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t x_stride,
