@@ -30,29 +30,30 @@ struct NormArgs {
     float eps;
 };
 
-// Sum and maximum over a team of TEAM threads, the same in all of them.
-template <int TEAM>
-__device__ __forceinline__ void team_reduce(float &s, uint32_t &m, float *lds)
+// Sum or maximum of a team of TEAM threads, the same in all of them.  `lds` has
+// a place per wave; a caller that uses it again lets the block meet in between.
+template <int TEAM, typename V, typename F>
+__device__ __forceinline__ V team_join(V mine, V *lds, F &&join)
 {
-    s = wave_sum(s);
-    m = wave_max(m);
     if constexpr (TEAM > 64) {
         constexpr int W = TEAM / 64;
-        const int w = threadIdx.x >> 6;
-        __syncthreads();                    // the last use of lds is over
-        if ((threadIdx.x & 63) == 0) {
-            lds[w] = s;
-            lds[W + w] = __builtin_bit_cast(float, m);
-        }
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = mine;
         __syncthreads();
-        s = 0.f;
-        m = 0;
+        mine = lds[0];
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            s += lds[i];
-            m = max(m, __builtin_bit_cast(uint32_t, lds[W + i]));
-        }
+        for (int i = 1; i < W; ++i) mine = join(mine, lds[i]);
     }
+    return mine;
+}
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float s, float *lds)
+{
+    return team_join<TEAM>(wave_sum(s), lds, [](float a, float b) { return a + b; });
+}
+template <int TEAM>
+__device__ __forceinline__ uint32_t team_max(uint32_t m, uint32_t *lds)
+{
+    return team_join<TEAM>(wave_max(m), lds, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // Eight codes from t c: adding 1.5 2^23 rounds to a whole number (to even) and
@@ -75,7 +76,8 @@ __device__ __forceinline__ u32x2 codes8(const float (&t)[8], float c)
 template <typename T, int TEAM, int NV, bool NORM, bool EIGHT>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
 {
-    __shared__ float lds[TEAM > 64 ? TEAM / 32 : 1];
+    __shared__ float sums[TEAM / 64];
+    __shared__ uint32_t tops[TEAM / 64];
     const int tid = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
     int64_t row = blockIdx.x;
     if constexpr (TEAM == 64) {
@@ -111,41 +113,40 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm(NormArgs a)
 #pragma unroll
         for (int v = 0; v < NV; ++v) load_any8(a.weight, a.w_dtype, tid + v * TEAM, cols, w[v]);
     }
-    float rstd = 1.f, ss = 0.f;
-    uint32_t top = 0;                       // the largest |h weight|, as its bits: NaN above infinity above all others
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (NORM) {
-                ss = __builtin_fmaf(t[v][e], t[v][e], ss);
-                if constexpr (EIGHT) {
-                    t[v][e] *= w[v][e];
-                    top = max(top, __builtin_bit_cast(uint32_t, t[v][e]) & 0x7fffffffu);
-                }
-            } else {
-                top = max(top, __builtin_bit_cast(uint32_t, t[v][e]) & 0x7fffffffu);
-            }
-        }
-    team_reduce<TEAM>(ss, top, lds);
     if constexpr (NORM) {
-        rstd = 1.f / __builtin_sqrtf(ss / static_cast<float>(cols) + a.eps);
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(t[v][e], t[v][e], ss);
+        ss = team_sum<TEAM>(ss, sums);
+        const float rstd = 1.f / __builtin_sqrtf(ss / static_cast<float>(cols) + a.eps);
         if (a.rstd && tid == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[v][e] = t[v][e] * rstd * w[v][e];
     }
     if constexpr (!EIGHT) {
         T *y = static_cast<T *>(a.y) + row * a.y_st;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[v][e] = t[v][e] * rstd * w[v][e];
-            store_row8<T>(y, tid + v * TEAM, cols, t[v]);
-        }
+        for (int v = 0; v < NV; ++v) store_row8<T>(y, tid + v * TEAM, cols, t[v]);
         return;
     }
-    float scale = fmaxf(__builtin_bit_cast(float, top) * rstd * (1.f / 127.f), kMinKvScale);
+    // The scale and the codes are those of y itself, which costs a second
+    // reduction.  One for both, of |h weight| with rstd behind it, would take
+    // other codes between two of them and overflow where y does not (16384 x 4096
+    // in bf16 81.9 us with either, 16384 x 576 16.4 against 15.8).
+    uint32_t top = 0;                       // the largest |y|, as its bits: NaN above infinity above all others
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, t[v][e]) & 0x7fffffffu);
+    top = team_max<TEAM>(top, tops);
+    float scale = fmaxf(__builtin_bit_cast(float, top) * (1.f / 127.f), kMinKvScale);
     if (top >= 0x7f800000u) scale = __builtin_nanf("");
     if (tid == 0) a.scale[row] = scale;
-    const float c = rstd / scale;           // codes of t = h weight (or x) in one product
+    const float c = 1.f / scale;
     int8_t *q = a.q + row * a.q_st;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -176,7 +177,7 @@ struct NormBwdArgs {
 template <typename T, int TEAM, int NV>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArgs a)
 {
-    __shared__ float lds[TEAM > 64 ? TEAM / 32 : 1];
+    __shared__ float lds[TEAM / 64];
     const int tid = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
     const int64_t teams = static_cast<int64_t>(gridDim.x) * (TEAM == 64 ? 4 : 1);
     int64_t team = blockIdx.x;
@@ -208,7 +209,6 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
         }
         const float rstd = a.rstd[row];
         float dot = 0.f;
-        uint32_t none = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float n[8], g[8];
@@ -227,8 +227,8 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
                 dot = __builtin_fmaf(p, w[WIDE ? 0 : v][e], dot);
             }
         }
-        team_reduce<TEAM>(dot, none, lds);
-        const float c = dot * inv;
+        if constexpr (TEAM > 64) __syncthreads();       // the last row's sums have been read
+        const float c = team_sum<TEAM>(dot, lds) * inv;
         T *dx = static_cast<T *>(a.dx) + row * a.dx_st;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {

@@ -738,15 +738,15 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
  * and one fp32 scale, standing for y^ = scale[m] q:
  *   scale = max(max_j |y_j| fl32(1/127), 2^-60),   q_j = rint(y_j / scale)
  * in fp32 (the quotient as a product with the reciprocal), rint to even.  A
- * row that holds a NaN or an infinity has a NaN scale, and so no values.
+ * row y that holds a NaN or an infinity has a NaN scale, and so no values.
  */
 
 /* pq_rmsnorm -- root-mean-square norm, with the residual's addition and an
  * output in 8 bits on request:
  *   h = x + residual (rounded to the type; x itself without a residual)
- *   y = h rstd weight,   rstd = (mean_j h_j^2 + eps)^(-1/2)
- * in fp32 (a row whose squares add up to 2^128 and more has rstd 0), y rounded
- * once -- to the type, or to 8 bits as above.
+ *   y = (h rstd) weight,   rstd = (mean_j h_j^2 + eps)^(-1/2)
+ * in fp32 (a row whose squares add up to 2^128 and more has rstd 0); this y is
+ * rounded to the type, or given in 8 bits as above.
  *   dtype      of x, residual, sum and y: PQ_F32, PQ_BF16 or PQ_F16
  *   rows       at most 2^31 - 1;  cols 1 .. 32768
  *   residual   in [rows, cols], or NULL;  sum out h, required with it (NULL
