@@ -119,22 +119,28 @@ __device__ __forceinline__ void read_entries(const DistillArgs &a, int64_t r, co
     if (!chains) return;
     lanes_agree();
     // A word that is named more than once: its first entry takes the sum.  It
-    // is one of whole numbers (of 2^-50; the list's largest p is 1), so that
-    // the chain's order, which is chance, does not show.
+    // is one of whole numbers (of 2^-50 of the word's largest p), so that the
+    // chain's order, which is chance, does not show.
     for (int j = lane; j < a.k; j += 64) {
         float p = l.p[j];
         if (p == 0.f) continue;
         const int w = l.word[j];
         bool first = true, more = false;
-        uint64_t sum = 0;
+        float most = p;
         for (int i = l.head[(w >> 3) & (kHeads - 1)]; i >= 0; i = l.next[i]) {
             if (l.word[i] != w) continue;
             first = first && i >= j;
             more = more || i != j;
-            sum += static_cast<uint64_t>(static_cast<double>(l.p[i]) * 0x1p50);
+            most = fmaxf(most, l.p[i]);
         }
-        if (more) p = first ? static_cast<float>(static_cast<double>(sum) * 0x1p-50) : 0.f;
-        l.all[j] = p;
+        if (more && first) {
+            const int e = __builtin_amdgcn_frexp_expf(most);        // most < 2^e: 1024 terms stay below 2^60
+            uint64_t sum = 0;
+            for (int i = l.head[(w >> 3) & (kHeads - 1)]; i >= 0; i = l.next[i])
+                if (l.word[i] == w) sum += static_cast<uint64_t>(ldexp(static_cast<double>(l.p[i]), 50 - e));
+            p = static_cast<float>(ldexp(static_cast<double>(sum), e - 50));
+        }
+        l.all[j] = first ? p : 0.f;
     }
 }
 
