@@ -2,7 +2,8 @@
 // from a teacher's top logits, and its gradient.
 //
 // Per row: q = softmax(z / T) over the vocabulary, p = softmax(t / T) over the
-// k entries of the teacher, loss = T^2 sum p (ln p - ln q), dz = T (q - p).
+// k entries of the teacher, loss = T^2 sum p (ln p - ln q) over the entries, dz =
+// T (q - P) with P the entries' p summed by word.
 // Two exponentials and a handful of operations a word on 2 to 8 bytes of
 // traffic: the memory system bounds it.  One block takes a row.  Each thread
 // sums exp against the maximum of its own words and the (maximum, sum) pairs

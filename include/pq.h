@@ -842,13 +842,18 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
 /*
  * pq_distill -- distillation from a teacher's top logits.  Row r's teacher
  * gives logits top[r, j] at words index[r, j], j < k; with temperature T
- *   p = softmax_j(top[r, j] / T) over the entries with an index in
- *       [0, vocab) (others do not count; a word that is named twice has the
- *       sum of both),   q = softmax_i(logits[r, i] / T) over all words
+ *   p_j = softmax_j(top[r, j] / T) over the entries with an index in
+ *         [0, vocab) (others do not count)
+ *   q = softmax_i(logits[r, i] / T) over all words
  *   loss[r] = row_weight[r] T^2 sum_j p_j (ln p_j - ln q_index[j])
- *   dlogits[r, i] = grad_scale row_weight[r] T (q_i - p_i)
+ *   dlogits[r, i] = grad_scale row_weight[r] T (q_i - P_i)
+ *   P_i = the sum of the p_j with index[r, j] = i, 0 for other words
  * i.e. the gradient of grad_scale * sum_r loss[r], computed while the row is
- * at hand.  A row of weight 0, or without an entry that counts and is above
+ * at hand.  Where every word is named once the loss is the divergence of q from
+ * p.  A word that is named again counts entry by entry in the loss, which is
+ * then lower than the divergence from P by T^2 (sum_i P_i ln P_i -
+ * sum_j p_j ln p_j), a number that does not depend on the logits (and may
+ * make the loss negative); the gradient is that of both.  A row of weight 0, or without an entry that counts and is above
  * -inf, has loss 0 and gradient 0, whatever its logits hold (and stats (0, 1));
  * an entry of p_j = 0 adds nothing to the loss.
  * A logit of -inf has q_i = 0; NaN, +inf and rows of nothing but -inf give NaN.
@@ -870,7 +875,7 @@ pq_status pq_distill(int dtype, int64_t rows, int64_t vocab, const void *logits,
                      int64_t d_stride, void *stream);
 
 /* pq_distill_bwd -- the gradient by itself, for losses that are weighed later:
- * dlogits[r, i] = dloss[r] row_weight[r] T (q_i - p_i), from the stats of
+ * dlogits[r, i] = dloss[r] row_weight[r] T (q_i - P_i), from the stats of
  * pq_distill on the same logits.  dlogits may be logits. */
 pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *logits, int64_t l_stride, int64_t k,
                          const int32_t *index, const void *top, int top_dtype, double temperature,

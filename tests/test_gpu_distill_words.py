@@ -1,4 +1,6 @@
-"""Words that a teacher's list of pq_distill names more than once: the gradient's sum over them at every size."""
+"""Words that a teacher's list of pq_distill names more than once: the gradient's sum over them at every size, the loss by entries."""
+import math
+
 import pytest
 import torch
 
@@ -41,3 +43,18 @@ def test_small_sums(pq, times, temp):
     again = torch.empty_like(z)
     pq.pq_distill(z, index, top, dlogits=again, temperature=temp)
     assert torch.equal(again, dz)
+
+
+@pytest.mark.parametrize("k", [1, 2, 40])
+def test_loss_counts_entries(pq, k):
+    """One word k times: every entry has p = 1 / k, so the loss is T^2 (-ln k - ln q); the gradient's p is 1."""
+    z = torch.randn(3, 500, generator=torch.Generator().manual_seed(k)).to(DEV)
+    index, top = torch.full((3, k), 9, dtype=torch.int32, device=DEV), torch.full((3, k), 2.5, device=DEV)
+    loss, dz = torch.empty(3, device=DEV), torch.empty_like(z)
+    pq.pq_distill(z, index, top, loss, dlogits=dz, temperature=2.0)
+    log_q = torch.log_softmax(z.double() / 2, -1)
+    want = 4 * (-math.log(k) - log_q[:, 9])
+    assert bool(((loss.double() - want).abs() <= 4 * 2.0 ** -18 * (1 + math.log(k) + log_q[:, 9].abs())).all())
+    p = torch.zeros_like(log_q)
+    p[:, 9] = 1
+    assert bool(((dz.double() - 2 * (log_q.exp() - p)).abs() <= 2 * (p + log_q.exp()) * 2.0 ** -17).all())
