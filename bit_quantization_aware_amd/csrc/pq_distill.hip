@@ -399,6 +399,7 @@ inline pq_status distill_args(DistillArgs &a, int dtype, int64_t rows, int64_t v
         misaligned(row_weight, 4))
         return PQ_ERR_ALIGN;
     if (dlogits == logits && d_stride != l_stride) return PQ_ERR_ARG;
+    if (dlogits && rows_overlap(rows, vocab, d_stride)) return PQ_ERR_SHAPE;
     a.z = logits;
     a.top = top;
     a.dz = dlogits;

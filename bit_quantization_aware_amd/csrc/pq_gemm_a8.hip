@@ -657,6 +657,7 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
         return PQ_ERR_ALIGN;
     if (workspace_bytes < 0 || (need > 0 && workspace_bytes < need)) return PQ_ERR_ARG;
     if (e.other && e.other == Y && e.other_stride != y_stride) return PQ_ERR_ARG;
+    if (rows_overlap(M, N, y_stride)) return PQ_ERR_SHAPE;
     A8Args a = {};
     a.X = X;
     a.x_scale = x_scale;

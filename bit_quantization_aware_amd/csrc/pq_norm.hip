@@ -407,6 +407,7 @@ pq_status pq_rmsnorm(int dtype, int64_t rows, int64_t cols, const void *x, int64
     if ((sum == x && s_stride != x_stride) || (sum && sum == residual && s_stride != r_stride) ||
         (y && y == x && y_stride != x_stride) || (y && y == sum))
         return PQ_ERR_ARG;
+    if ((sum && rows_overlap(rows, cols, s_stride)) || rows_overlap(rows, cols, y ? y_stride : q_stride)) return PQ_ERR_SHAPE;
     NormArgs a = {};
     a.x = x;
     a.residual = residual;
@@ -456,6 +457,7 @@ pq_status pq_rmsnorm_bwd(int dtype, int64_t rows, int64_t cols, const void *h, i
     if (dweight && workspace_bytes < pq_rmsnorm_bwd_workspace_bytes(rows, cols)) return PQ_ERR_ARG;
     if (rows > 0 && ((dx == dy && dx_stride != dy_stride) || (dx == dsum && dx_stride != ds_stride) || dx == h))
         return PQ_ERR_ARG;
+    if (rows_overlap(rows, cols, dx_stride)) return PQ_ERR_SHAPE;
     if (rows > 0) {
         NormBwdArgs a = {};
         a.h = h;
@@ -495,6 +497,7 @@ pq_status pq_quantize_rows(int dtype, int64_t rows, int64_t cols, const void *x,
     if (rows == 0) return PQ_OK;
     if (!x || !q || !scale) return PQ_ERR_NULL;
     if (misaligned(x, size) || misaligned(scale, 4)) return PQ_ERR_ALIGN;
+    if (rows_overlap(rows, cols, q_stride)) return PQ_ERR_SHAPE;
     NormArgs a = {};
     a.x = x;
     a.q = q;

@@ -104,6 +104,9 @@ inline void skip_rows(P *&p, int64_t rows, int64_t stride, int size)
     if (p) p = reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(rows * stride * size));
 }
 
+// Whether the rows of an output would lie over each other.
+inline bool rows_overlap(int64_t rows, int64_t cols, int64_t stride) { return rows > 1 && stride < cols && stride > -cols; }
+
 // Eight values of an array of any element type (a run-time choice that is the
 // same for all threads).
 __device__ __forceinline__ void load_any8(const void *a, int dtype, int c, int cols, float (&x)[8])

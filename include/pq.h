@@ -731,7 +731,10 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
  * contiguous, sizes of zero enqueue nothing); matrices need the alignment of
  * their elements only, unless said otherwise, and scales, statistics and
  * losses are fp32.  An output may be the same array as an input where that is
- * said (same address, same stride); any other overlap is not allowed.  For
+ * said (same address, same stride); any other overlap is not allowed, and an
+ * output of more than one row whose stride is less than a row (in size: it may
+ * be negative) is PQ_ERR_SHAPE.  Inputs may have any stride, 0 too, unless said
+ * otherwise.  For
  * fixed arguments every result is the same in every run.
  *
  * Rows in 8 bits: row m of a matrix y is held as int8 codes q in -127 .. 127
