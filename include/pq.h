@@ -788,7 +788,9 @@ pq_status pq_quantize_rows(int dtype, int64_t rows, int64_t cols, const void *x,
 
 /* Activations of the product's epilogue: none, max(v, 0), v / (1 + e^-v),
  * v (1 + erf(v / sqrt 2)) / 2, and the latter's tanh form
- * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2. */
+ * v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2.  In fp32, where they are
+ * small too: an activation that makes v smaller by e^-u has a relative error of
+ * at most 2^-24 (12 + 9 u). */
 #define PQ_ACT_NONE 0
 #define PQ_ACT_RELU 1
 #define PQ_ACT_SILU 2
