@@ -468,9 +468,8 @@ pq_status pq_distill_bwd(int dtype, int64_t rows, int64_t vocab, const void *log
     a.dloss = dloss;
     a.grad = temperature;
     const int64_t chunks = vocab / 8 > 0 ? vocab / 8 : 1;
-    // up to 65535 blocks a row, of 32768 words and more
-    int64_t segments = (chunks + 4095) / 4096;
-    if (segments > 65535) segments = 65535;
+    // equal parts of up to 32768 words, at most 32768 of them a row
+    const int64_t segments = (chunks + 4095) / 4096;
     a.segment = static_cast<int>((chunks + segments - 1) / segments);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     auto with = [&](auto type) {

@@ -734,8 +734,7 @@ pq_status pq_attn_decode(const pq_kv_cache *cache, int q_dtype, int64_t batch, i
  * said (same address, same stride); any other overlap is not allowed, and an
  * output of more than one row whose stride is less than a row (in size: it may
  * be negative) is PQ_ERR_SHAPE.  Inputs may have any stride, 0 too, unless said
- * otherwise.  For
- * fixed arguments every result is the same in every run.
+ * otherwise.  For fixed arguments every result is the same in every run.
  *
  * Rows in 8 bits: row m of a matrix y is held as int8 codes q in -127 .. 127
  * and one fp32 scale, standing for y^ = scale[m] q:
@@ -808,7 +807,7 @@ typedef struct pq_epilogue {
     int64_t other_stride; /* elements between its rows                      */
     int32_t bias_dtype;   /* PQ_F32, PQ_BF16, PQ_F16                        */
     int32_t activation;   /* PQ_ACT_..                                      */
-    int32_t combine;      /* PQ_COMBINE_.. (without `other`: not used)      */
+    int32_t combine;      /* PQ_COMBINE_.. (0 is right without `other`)     */
     int32_t reserved;     /* 0                                              */
 } pq_epilogue;
 
