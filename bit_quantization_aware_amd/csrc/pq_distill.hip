@@ -414,10 +414,13 @@ inline pq_status distill_args(DistillArgs &a, int dtype, int64_t rows, int64_t v
     a.temp = temp;
     a.inv_temp = inv;
     a.c = c;
-    // Half the memory-side cache's size and more is written past the caches
-    // (2048 x 128256 in bf16 208 us against 218, 512 x 200000 103 against 119);
-    // less may be found there by its reader (517 x 32003 in fp32 28 against 41).
-    a.nt = rows * vocab * size > (int64_t(1) << 27);
+    // Over half the memory-side cache's size is written past the caches (2048 x
+    // 128256 in bf16 209 us against 220, 512 x 200000 95 against 109); less may be
+    // found there by its reader.  Not where a store is part of a piece of memory:
+    // fp32, whose eight words take two (1024 x 128256 280 against 242), and rows at
+    // odd addresses (2048 x 128257 264 against 261, the gradient alone 243 against
+    // 229).
+    a.nt = size == 2 && rows * vocab * size > (int64_t(1) << 27) && aligned16(dlogits) && d_stride % 8 == 0;
     return PQ_OK;
 }
 

@@ -684,7 +684,8 @@ pq_status pq_gemm_a8(int mode, int64_t M, int64_t N, int64_t K, const int8_t *X,
     a.splits = plan.splits;
     a.p_st = plan.p_st;
     // An output of half the memory-side cache's size and more is not written
-    // into the caches.
+    // into the caches (16384 x 14336 x 576 in bf16 190 us against 198, in fp32 272
+    // against 281; 8192 x 14336 x 4096 with a second operand 410 against 416).
     a.nt = M * N * size >= (int64_t(1) << 27);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const int bits = code_bits(mode);

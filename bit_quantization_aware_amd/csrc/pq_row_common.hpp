@@ -59,9 +59,13 @@ __device__ __forceinline__ Raw8<T> load_row8(const T *row, int c, int cols)
     return r;
 }
 
+// NT: past the caches.  Where a branch has this store on one side and an
+// ordinary one on the other, the compiler would make one of the two and drop the
+// hint; it cannot join what lies between statements of its own.
 template <bool NT = false, typename T>
 __device__ __forceinline__ void store_whole8(T *p, const float (&x)[8])
 {
+    if constexpr (NT) asm volatile("");
     if constexpr (sizeof(T) == 4) {
         const f32x4 v[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
         f32x4_a4 *to = reinterpret_cast<f32x4_a4 *>(p);
@@ -78,6 +82,7 @@ __device__ __forceinline__ void store_whole8(T *p, const float (&x)[8])
         if constexpr (NT) __builtin_nontemporal_store(v, to);
         else *to = v;
     }
+    if constexpr (NT) asm volatile("");
 }
 
 template <typename T, bool NT = false>
