@@ -10,10 +10,10 @@
 // are joined once, so there is one reduction a row; rows of up to 131072 words
 // of 16 bits (65536 of fp32) stay in registers between the sum and the
 // gradient, what longer ones have more is read a second time (1024 rows of 128256
-// words in fp32 239 us; 293 with all of it read twice).  One wave reads the teacher's
-// list while the others read the row.
-// 2048 rows of 128256 words in bf16 take 208 us, 5.06 TB/s, the rate of a copy;
-// the gradient by itself 206.
+// words in fp32 242 us; 288 with nearly all of it read twice).  One wave reads the
+// teacher's list while the others read the row.
+// 2048 rows of 128256 words in bf16 take 210 us, 5.0 TB/s, the rate of a copy; the
+// loss by itself 112, the gradient 206.
 //
 // p is 0 for all but k words.  The entries stand in LDS as chains hashed by
 // chunks of eight words: a thread looks at one head per chunk and walks a
@@ -334,10 +334,11 @@ __global__ __launch_bounds__(512) void k_distill_bwd(DistillArgs a)
     if (rest >= 0 && rest < a.vocab) grad1<T>(a, l, dz, rest, to_f32(z[rest]), top, gq, gp);
 }
 
-// Threads and chunks by the row.  (For the loss alone rows over 65536 words would
-// be read faster past the registers, with two blocks a CU in place of one: 2048
-// rows of 128256 words in bf16 93 us against 108; with the gradient 262 against
-// 218.  One form for both gives one loss, bit for bit.)
+// Threads and chunks by the row.  (With eight chunks for rows over 65536 words, two
+// blocks a CU in place of one, and the rest of the row read twice, 2048 rows of
+// 128256 words in bf16 take 210 us with a gradient that goes past the caches, as
+// with sixteen, 235 against 218 with one that does not, and 94 against 112 for the
+// loss alone.  One form for all gives one loss, bit for bit.)
 template <typename T>
 pq_status launch_rows(const DistillArgs &a, hipStream_t s)
 {

@@ -192,8 +192,9 @@ __global__ __launch_bounds__(64 * WN * KG, 2) void k_a8_tile(A8Args a, int mtile
     const int w = KG == 1 ? wave : wave % WN, kg = KG == 1 ? 0 : wave / WN;
     const int i16 = lane & 15, g = lane >> 4;
 
-    // One XCD's blocks take consecutive tiles, eight row tiles by all columns
-    // at a time, so that its L2 serves both operands.
+    // Tiles go eight row tiles by all columns at a time.  Where the number of
+    // blocks is a multiple of eight, one XCD's blocks take consecutive ones, so
+    // that its L2 serves both operands; other launches deal them round the XCDs.
     int t = blockIdx.x;
     const int nb = gridDim.x;
     if ((nb & 7) == 0) t = (t & 7) * (nb >> 3) + (t >> 3);
@@ -494,7 +495,10 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
 // How a shape is cut.  Up to 16 rows the stream kernel; up to 32 too (at 2 and 4
 // bits: 32 rows of 14336 x 4096 9.0 us, of 1600 x 4352 7.3, in tiles 11.8 and 9.8),
 // but for long K under few columns, where every one-tile block reads all
-// activations (32 rows of a 4-bit 4096 x 14336 16.8 us, in tiles 15.0).
+// activations (32 rows of a 4-bit 4096 x 14336 16.8 us, in tiles 15.0).  At 1 bit
+// a group of 32 rows' activations is 16 loads, for which the ring has room with two
+// waves only (32 rows of 14336 x 4096 9.9 us, of 1600 x 4352 6.0; in tiles 9.0 and
+// 9.2): there is no such form.
 // 128 x 256 tiles from 176 of them on (512 rows of 14336 x
 // 4096, 224 tiles: 33 us against 40; 333 rows, 168 tiles: 34 both ways; 256 rows,
 // 112 tiles: 31 against 21).  Else 64 x 128, of one group of waves
@@ -504,9 +508,10 @@ __global__ __launch_bounds__(256) void k_a8_join(A8Args a)
 // that 32 x 64, two waves and two groups, two blocks a CU (64 rows of N = K = 4096
 // 8.4 us, 128 rows with 4 bits 8.6, 200 rows of 1600 x 4352 8.9, 40 of 576 x 576
 // 4.7; as 32 x 128, one a CU, 10.5, 10.9, 11.2 and 5.5), with K split while that
-// pays: a stage takes 0.13 us, a second launch and the way of the partial sums
-// 3 us and their 8 bytes at 4 TB/s (64 rows of 4096 x 14336 27 us in one share,
-// 14.5 in four).
+// pays: a second launch and the way of the partial sums take 3 us and their 8
+// bytes at 4 TB/s; a stage takes 0.15 us, and one less in each of the shares, which
+// run side by side, is counted with 0.125 (64 rows of 4096 x 14336 20.9 us in one
+// share, 14.8 in four, where this expects 15.5; of 4096 x 28672 37.9, 20.3 and 22).
 struct A8Plan {
     int mt, groups;          // 16-row tiles a block (0: the stream kernel), groups of waves
     int splits;              // shares of K
@@ -582,6 +587,9 @@ pq_status launch_a8(const A8Args &a, const A8Plan &plan, hipStream_t s)
         if constexpr (RPL <= 2) return launch_stream<BITS, 8>(a, s);
         if constexpr (RPL > 2) return launch_stream<BITS, 32 / RPL, 2>(a, s);
     }
+    // The large tile's ring has the slots that let two blocks share a CU's LDS, at 4
+    // bits two: with three the 8192 x 14336 x 4096 of 3 and 4 bits take 502 and 494
+    // us, with two 404 and 417 (2 bits 407 with either).
     if (plan.mt == 2) return launch_tile<BITS, 2, 2, 2, 2, 4>(a, s);
     if (plan.mt == 4 && plan.groups == 2) return launch_tile<BITS, 4, 2, 4, 2, 3>(a, s);
     if (plan.mt == 4) return launch_tile<BITS, 4, 1, 4, 2, 4>(a, s);

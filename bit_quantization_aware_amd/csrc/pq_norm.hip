@@ -184,7 +184,8 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_norm_bwd(NormBwdArg
     if constexpr (TEAM == 64) team = team * 4 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int cols = a.cols;
     const float inv = 1.f / static_cast<float>(cols);
-    // A block of 1024 threads has 128 registers a thread: the weight is read
+    // A block of 1024 threads has 128 registers a thread (with four chunks too few:
+    // 37 are spilled, 90 in fp32; 2048 x 32768 174 us, in fp32 341): the weight is read
     // again for every row there (from the caches), dsum after the row's sum.
     constexpr bool WIDE = TEAM == 1024;
     float w[WIDE ? 1 : NV][8], dw[NV][8];
@@ -359,7 +360,8 @@ pq_status launch_norm(NormArgs a, hipStream_t s)
 // Blocks of the gradient, each with a row of partial sums: two of 256 threads a
 // CU and four of waves that take a row each (16384 x 4096 in bf16 with 256, 512,
 // 768, 1024 blocks 116, 103, 107, 111 us; 65536 x 576 with 512, 1024, 1792,
-// 2048 99, 68, 76, 71).
+// 2048 99, 68, 76, 71), one of 1024 threads (2048 x 16384 with 128, 256, 512 blocks
+// 94, 69, 76; 2048 x 32768 245, 174, 201).
 inline int64_t bwd_blocks(int64_t rows, int64_t cols)
 {
     const int team = team_of(cols);
